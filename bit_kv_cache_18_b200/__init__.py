@@ -53,6 +53,17 @@ class WindowDesc(ctypes.Structure):
                 ("sink", ctypes.c_int32), ("recent", ctypes.c_int32)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_len", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class ScoreOpts(ctypes.Structure):
+    _fields_ = [("softmax_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p)]
+
+
 def lib():
     """Load libkvq.so (raises if it is absent: there is no other path)."""
     global _lib
@@ -88,6 +99,14 @@ def lib():
                 "kvq_decode_attention_window": (ctypes.c_int, [dp, ctypes.POINTER(WindowDesc), vp, ctypes.c_int, i32,
                                                                i32, vp, i32, vp, i32, f32, vp, ctypes.c_int, vp, sz,
                                                                vp]),
+                "kvq_update_tables": (ctypes.c_int, [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp,
+                                                     vp]),
+                "kvq_rope_table": (ctypes.c_int, [ctypes.POINTER(RopeDesc), vp, vp]),
+                "kvq_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), vp, f32, vp, i32, vp, i64, vp, i64, i32, vp,
+                                            i64, vp, i64, i32, ctypes.c_int, vp]),
+                "kvq_decode_scored_workspace_bytes": (sz, [dp, i32, i32, i32, i32]),
+                "kvq_decode_attention_scored": (ctypes.c_int, [dp, ctypes.POINTER(ScoreOpts), vp, ctypes.c_int, i32,
+                                                               i32, vp, i32, vp, i32, vp, ctypes.c_int, vp, sz, vp]),
                 "kvq_last_device_status": (ctypes.c_int, [vp]),
                 "kvq_error_string": (ctypes.c_char_p, [ctypes.c_int]),
             }
@@ -302,6 +321,167 @@ def kvq_decode_attention_window(pool, num_blocks, num_kv_heads, window, sink, re
                                            softmax_scale, _ptr(out), _dtype_code(out), _ptr(workspace),
                                            workspace.numel(), _stream_ptr(stream))
     _check(rc, "kvq_decode_attention_window")
+
+
+# ---- a serving step around the cache --------------------------------------------
+
+def _require(ok: bool, what: str):
+    """Argument rules that only the tensors show (shape, type, layout, device):
+    refused like the library's own, before anything is launched."""
+    if not ok:
+        raise KvqError(KVQ_ERR_INVALID, what)
+
+
+def _require_on_device(what: str, *tensors):
+    """Every tensor on the current CUDA device, where the launch goes."""
+    import torch
+    dev = torch.cuda.current_device()
+    _require(all(t is None or (t.is_cuda and t.device.index == dev) for t in tensors),
+             f"{what}: a tensor is not on the current CUDA device")
+
+
+def _require_int32(what: str, *tensors):
+    import torch
+    _require(all(t is None or (t.dtype == torch.int32 and t.is_contiguous()) for t in tensors),
+             f"{what}: tables and lengths are contiguous int32 tensors")
+
+
+def _require_rows(what: str, *tensors):
+    """[n, heads, 128] with contiguous rows."""
+    _require(all(t is None or (t.dim() == 3 and t.shape[2] == HEAD_DIM and
+                               (t.numel() == 0 or (t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == HEAD_DIM))))
+                 for t in tensors), f"{what}: rows are [tokens, heads, {HEAD_DIM}] with contiguous heads")
+
+
+def _row_stride(t) -> int:
+    """Elements from one token's row to the next (any value does for a single row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+
+
+def kvq_update_tables(ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens, positions,
+                      seq_ids, slots, stream=None):
+    """Block tables and slot maps of a step from its request lengths: int32
+    device tensors ring [capacity], state_in and state_out [4], seq_lens,
+    target_lens and lens_out [batch], block_table [batch, max_blocks],
+    cu_seqlens [batch + 1], positions, seq_ids and slots [max_tokens]."""
+    what = "kvq_update_tables"
+    batch, n = seq_lens.numel(), positions.numel()
+    _require_on_device(what, ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens,
+                       positions, seq_ids, slots)
+    _require_int32(what, ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens,
+                   positions, seq_ids, slots)
+    _require(state_in.numel() >= 4 and state_out.numel() >= 4 and target_lens.numel() == batch and
+             lens_out.numel() == batch and block_table.dim() == 2 and block_table.shape[0] == batch and
+             cu_seqlens.numel() == batch + 1 and seq_ids.numel() == n and slots.numel() == n,
+             f"{what}: buffer sizes")
+    rc = lib().kvq_update_tables(_ptr(ring), ring.numel(), _ptr(state_in), _ptr(state_out), _ptr(seq_lens),
+                                 _ptr(target_lens), _ptr(lens_out), batch, _ptr(block_table), block_table.shape[1],
+                                 _ptr(cu_seqlens), n, _ptr(positions), _ptr(seq_ids), _ptr(slots),
+                                 _stream_ptr(stream))
+    _check(rc, what)
+
+
+ROPE_SCALINGS = ("none", "linear", "ntk", "bands", "yarn")
+
+
+def make_rope(rotary_dim=HEAD_DIM, base=10000.0, interleaved=False, scaling="none", factor=1.0, original_len=0,
+              low=0.0, high=0.0) -> RopeDesc:
+    _require(scaling in ROPE_SCALINGS, "make_rope: scaling")
+    return RopeDesc(rotary_dim, int(interleaved), ROPE_SCALINGS.index(scaling), original_len, base, factor, low, high)
+
+
+def kvq_rope_table(desc: RopeDesc):
+    """-> (uint64 numpy [rotary_dim / 2]: turns per position in units of 2^-64, magnitude)"""
+    import numpy as np
+    turns = np.zeros(max(desc.rotary_dim // 2, 1), dtype=np.uint64)
+    mag = ctypes.c_float()
+    _check(lib().kvq_rope_table(ctypes.byref(desc), turns.ctypes.data, ctypes.byref(mag)), "kvq_rope_table")
+    return turns, mag.value
+
+
+def new_rope_table(desc: RopeDesc, device="cuda"):
+    """-> (the table on the device, as int64, magnitude)"""
+    import numpy as np
+    import torch
+    turns, mag = kvq_rope_table(desc)
+    return torch.from_numpy(turns.view(np.int64)).to(device), mag
+
+
+def kvq_rope(desc, table, magnitude, positions, q, k=None, q_out=None, k_out=None, stream=None):
+    """Rotate q [n, Hq, 128] and k [n, Hkv, 128] (fp16 or bf16) by positions
+    (int32 [n]) into q_out and k_out, in place where those are None."""
+    import torch
+    what = "kvq_rope"
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    _require((k is None) == (k_out is None), f"{what}: k_out without k")
+    n = positions.numel()
+    _require_on_device(what, table, positions, q, k, q_out, k_out)
+    _require_int32(what, positions)
+    _require_rows(what, q, k, q_out, k_out)
+    _require(table.dtype == torch.int64 and table.is_contiguous() and table.numel() == desc.rotary_dim // 2,
+             f"{what}: a table of another descriptor")
+    _require(q.shape[0] == n and q_out.shape == q.shape and q_out.dtype == q.dtype and
+             (k is None or (k.shape[0] == n and k_out.shape == k.shape and k.dtype == k_out.dtype == q.dtype)),
+             f"{what}: shapes and types")
+    hk = 0 if k is None else k.shape[1]
+    rc = lib().kvq_rope(ctypes.byref(desc), _ptr(table), magnitude, _ptr(positions), n, _ptr(q), _row_stride(q),
+                        _ptr(q_out), _row_stride(q_out), q.shape[1], _ptr(k), _row_stride(k) if hk else 0,
+                        _ptr(k_out), _row_stride(k_out) if hk else 0, hk, _dtype_code(q), _stream_ptr(stream))
+    _check(rc, what)
+
+
+def make_score_opts(softmax_scale=0.0, softcap=0.0, window=0, alibi_slopes=None) -> ScoreOpts:
+    """alibi_slopes: fp32 device tensor [num_q_heads], kept alive by the options."""
+    import torch
+    if alibi_slopes is not None:
+        _require(alibi_slopes.is_cuda and alibi_slopes.dtype == torch.float32 and alibi_slopes.is_contiguous(),
+                 "make_score_opts: alibi_slopes is a contiguous fp32 device tensor")
+    o = ScoreOpts(softmax_scale, softcap, window, alibi_slopes.data_ptr() if alibi_slopes is not None else None)
+    o.slopes_tensor = alibi_slopes
+    return o
+
+
+def _require_opts(what: str, opts, num_q_heads: int):
+    slopes = getattr(opts, "slopes_tensor", None)
+    _require_on_device(what, slopes)
+    _require(slopes is None or slopes.numel() == num_q_heads, f"{what}: one slope per query head")
+
+
+def kvq_decode_scored_workspace_bytes(num_blocks, num_kv_heads, batch, num_q_heads, max_seq_len, window=0,
+                                      preset=(4, 2)) -> int:
+    desc = make_desc(num_blocks, num_kv_heads, preset=preset)
+    return lib().kvq_decode_scored_workspace_bytes(ctypes.byref(desc), batch, num_q_heads, max_seq_len, window)
+
+
+def new_scored_workspace(num_blocks, num_kv_heads, batch, num_q_heads, max_seq_len, window=0, device="cuda",
+                         preset=(4, 2)):
+    import torch
+    n = kvq_decode_scored_workspace_bytes(num_blocks, num_kv_heads, batch, num_q_heads, max_seq_len, window, preset)
+    if n == 0 and batch > 0:
+        raise KvqError(KVQ_ERR_UNSUPPORTED, "kvq_decode_scored_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kvq_decode_attention_scored(pool, num_blocks, num_kv_heads, q, block_table, seq_lens, max_seq_len, out, workspace,
+                                opts, stream=None, preset=(4, 2)):
+    """kvq_decode_attention with score options (make_score_opts); workspace
+    from new_scored_workspace() with the same window."""
+    what = "kvq_decode_attention_scored"
+    desc = make_desc(num_blocks, num_kv_heads, pool, preset)
+    batch, hq, d = q.shape
+    _require_on_device(what, pool, q, block_table, seq_lens, out, workspace)
+    _require_int32(what, block_table, seq_lens)
+    _require(d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape and
+             block_table.dim() == 2 and block_table.shape[0] == batch and seq_lens.numel() == batch,
+             f"{what}: shapes and layout")
+    _require(pool.numel() * pool.element_size() >= kvq_cache_bytes(desc), f"{what}: pool too small")
+    _require_opts(what, opts, hq)
+    rc = lib().kvq_decode_attention_scored(ctypes.byref(desc), ctypes.byref(opts), _ptr(q), _dtype_code(q), batch, hq,
+                                           _ptr(block_table), block_table.shape[1], _ptr(seq_lens), max_seq_len,
+                                           _ptr(out), _dtype_code(out), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(rc, what)
 
 
 def kvq_selftest_wait_timeout(limit_us: int, elapsed_ns=None, stream=None):

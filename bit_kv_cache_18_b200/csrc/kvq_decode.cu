@@ -151,6 +151,7 @@ struct __align__(1024) Smem {
   int32_t tbl[kTblBlocks];                   // the split's block ids, -1 where absent (outside the split,
                                              // the sequence or the pool)
   float2 hq[8];                              // per head: sum(q~), max|q~|
+  float slope[8];                            // per head: distance bias per position, base 2 (score options)
   float red[R::kSoft][8][2];                 // cross-warp reductions
   float palpha[R::kSoft][8];                 // per softmax warp: factor of the pending O buffer
   float c1;                                  // max|q~| / 127: the unit of the query digits
@@ -815,9 +816,25 @@ __device__ __forceinline__ void window_part(const DecodeArgs& a, uint8_t* smem) 
   if (take_ticket(a, b, h, is_last)) merge_records<G, kThreads>(a, b, h);
 }
 
-// kWin: the instantiation that takes a bf16 window (a.win set); the others
-// carry no window code at all.
-template <int G, int KB, int VB, bool kWide, bool kWin>
+// Score options (kvq_score_opts): the base-2 score s of a token `dist`
+// positions before the newest becomes
+//   cap tanh(s / cap) - slope dist,
+// cap and slope in base-2 units too.  tanh(x) = 1 - 2 / (e^2x + 1) keeps an
+// absolute error of about 2^-22 cap in the score (e^2x = 0 and infinity give
+// -cap and cap), where the hardware's tanh approximation (2^-11) would cost a
+// softcap of 50 two percent of every probability.
+__device__ __forceinline__ float scored(const DecodeArgs& a, float s, float slope, float dist) {
+  if (a.softcap > 0.0f) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * a.softcap_exp) + 1.0f));
+    s = fmaf(-2.0f * a.softcap, r, a.softcap);
+  }
+  return fmaf(-slope, dist, s);
+}
+
+// kWin: the instantiation that takes a bf16 window (a.win set); kScore: the
+// one that takes score options.  The others carry no code of either.
+template <int G, int KB, int VB, bool kWide, bool kWin, bool kScore>
 __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf<KB, VB>)
     decode_kernel(DecodeArgs a) {
   using F = Fmt<KB, VB>;
@@ -886,8 +903,10 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
     // now is updated in L2, the point of coherence, by any later write): the
     // split's block-table slice, the sequence length and, by the block ids
     // as they read now, the first three chunks' segments.
+    // (With a sliding window the split's blocks follow from the length: no
+    // prefetch.)
     const int pblk0 = blockIdx.x * a.blocks_per_split;
-    const int pn = min(a.blocks_per_split, a.max_blocks_per_seq - pblk0);
+    const int pn = kScore && a.score_window > 0 ? 0 : min(a.blocks_per_split, a.max_blocks_per_seq - pblk0);
     const int32_t* prow = a.block_table + static_cast<int64_t>(blockIdx.z) * a.max_blocks_per_seq + pblk0;
     for (int ln = tid; ln * 32 < pn; ln += 32 * kLoadWarps) prefetch_line_l2(prow + ln * 32);
     if (tid == 0) prefetch_line_l2(a.seq_lens + blockIdx.z);
@@ -930,7 +949,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
         for (int k = 0; k < 4; ++k) x[i][k] = load_as_f32(a.q, a.q_dtype, q0 + lane + 32 * k);
       }
     }
-  } else if (warp == kMmaWarp && a.k_new != nullptr) {
+  } else if (!kScore && warp == kMmaWarp && a.k_new != nullptr) {
     const int64_t off = static_cast<int64_t>(b) * a.new_stride_bytes + static_cast<int64_t>(h) * (kHeadDim * 2) + 8 * lane;
     new_k = *reinterpret_cast<const uint2*>(a.k_new + off);
     new_v = *reinterpret_cast<const uint2*>(a.v_new + off);
@@ -943,11 +962,22 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   // the block ids of their segment of chunks 0 .. 2; the split's whole slice
   // of the row goes to shared memory in the set-up below, cut to the split
   // and the pool.
-  const int blk0 = split * a.blocks_per_split;
+  // With a sliding window the first split starts at the first block that holds
+  // a position of the window.  The score options walk the chunks from the
+  // newest to the oldest, since a distance bias makes scores fall with the
+  // distance: the running max is then found at once instead of moving with
+  // every chunk.
+  int blk0 = split * a.blocks_per_split;
+  if constexpr (kScore) {
+    if (a.score_window > 0) {
+      const int len = min(min(a.seq_lens[b], a.max_seq_len), a.max_blocks_per_seq * kBlockSize);
+      blk0 += max(len - a.score_window, 0) / kBlockSize;
+    }
+  }
   const int32_t* bt_row = a.block_table + static_cast<int64_t>(b) * a.max_blocks_per_seq;
   constexpr int kTblPer = kTblBlocks / (32 * kLoadWarps);
   int32_t bfirst[kNV];  // loaders, lanes sg < kSegs: block ids of chunks 0 .. 2
-  if (is_loader) {
+  if (!kScore && is_loader) {
     const int nload = min(a.blocks_per_split, a.max_blocks_per_seq - blk0);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -975,10 +1005,13 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
     qlo = min(a.win_sink, L);
     qhi = a.win_recent > 0 ? max(L - a.win_recent, qlo) : L;
   }
+  if constexpr (kScore) qlo = a.score_window > 0 ? max(L - a.score_window, 0) : 0;
   const int blk1 = min(min(nb, blk0 + a.blocks_per_split), (qhi + kBlockSize - 1) / kBlockSize);
   // a block holds positions read from the pool
   auto needed = [&](int blk) { return blk * kBlockSize < qhi && (blk + 1) * kBlockSize > qlo; };
   const int nchunks = blk1 > blk0 ? (blk1 - blk0 + kChunkBlocks - 1) / kChunkBlocks : 0;
+  // the chunk of the split that is walked c-th
+  auto chunk_of = [&](int c) { return kScore ? nchunks - 1 - c : c; };
   bool bad = false;      // a wait ran out: the results are void, the control flow is kept
   bool bad_blk = false;  // a block-table entry outside the pool (its tokens are skipped)
 
@@ -1004,7 +1037,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   // the chunk holding the block that the fused append writes is copied only
   // after the set-up barrier (-1: none)
   int c_defer = -1;
-  if (a.k_new != nullptr && L > 0 && !l_bad) {
+  if (!kScore && a.k_new != nullptr && L > 0 && !l_bad) {
     const int bn = (L - 1) / kBlockSize;
     if (bn >= blk0 && bn < blk1) c_defer = (bn - blk0) / kChunkBlocks;
   }
@@ -1012,8 +1045,16 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   if (is_loader) {
     // my block ids of chunks 0 .. 2, cut to the split and the pool
     const int nblk = blk1 - blk0;
+    if constexpr (kScore) {  // the last chunks: known only with the length
 #pragma unroll
-    for (int i = 0; i < kNV; ++i) {
+      for (int i = 0; i < kNV; ++i) {
+        const int j = kChunkBlocks * chunk_of(i) + seg_of<kWide>(warp, lane % kSegs);
+        bfirst[i] = lane < kSegs && i < nchunks && j < nblk ? __ldg(bt_row + blk0 + j) : -1;
+        if (!(bfirst[i] >= 0 && bfirst[i] < a.num_blocks && needed(blk0 + j))) bfirst[i] = -1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; !kScore && i < kNV; ++i) {
       const int j = kChunkBlocks * i + seg_of<kWide>(warp, lane % kSegs);
       if (!(j < nblk && needed(blk0 + j) && bfirst[i] >= 0 && bfirst[i] < a.num_blocks)) bfirst[i] = -1;
     }
@@ -1061,6 +1102,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
     for (int g = 0; g < G; ++g) mx = fmaxf(mx, sm.hq[g].y);
     const float inv = mx > 0.0f ? 127.0f / mx : 0.0f;
     if (st == 0) sm.c1 = mx * (1.0f / 127.0f);
+    if (kScore && st < G)
+      sm.slope[st] = a.alibi_slopes != nullptr ? __ldg(a.alibi_slopes + h * G + st) * 1.4426950408889634f : 0.0f;
 #pragma unroll
     for (int i = 0; i < kQHeads; ++i) {
       const int g = sw + kSoftWarps * i;
@@ -1084,7 +1127,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
       }
     }
     async_proxy_fence();
-  } else if (c_defer >= 0) {
+  } else if (!kScore && c_defer >= 0) {
     // fused one-token append: the MMA warp (idle until the first chunk
     // lands) of the split holding position L-1 writes the new token's K and
     // V of kv head h into that position, in parallel with the query
@@ -1158,7 +1201,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
         for (int i = 0; i < VB / 2; ++i) vr[sg][i] = lds128(sb + sg * kSeg + F::kOffV + 512 * i + 16 * lane);
       }
       const uint2 mr2 = lds64(sb + mslot * kSeg + F::kOffSK + 8 * (lane & 15));
-      const bool seg_ok = sm.tbl[kChunkBlocks * c + mblk] >= 0;  // my factor segment is present
+      const bool seg_ok = sm.tbl[kChunkBlocks * chunk_of(c) + mblk] >= 0;  // my factor segment is present
       // the slot is read: refill it with chunk c+3 (the reads above are
       // ordered before the copy's writes by the proxy fence).  (After a
       // failed wait no copy is issued any more: see the drain below.)  An
@@ -1168,7 +1211,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
       async_proxy_fence();
       __syncwarp();
       if (!bad && c + kNV < nchunks)
-        issue(lane < kSegs ? sm.tbl[kChunkBlocks * (c + kNV) + seg_of<kWide>(warp, lane)] : -1, r.i);
+        issue(lane < kSegs ? sm.tbl[kChunkBlocks * chunk_of(c + kNV) + seg_of<kWide>(warp, lane)] : -1, r.i);
 
       if (c >= kNV) {  // buffers r.i are free once PV(c-3) (issued after QK(c-2)) is done
         if (!mbar_wait<kWaitTag>(&sm.pv_done[r.i], r.ph ^ 1u, abort)) bad = true;
@@ -1203,7 +1246,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
          // (a segment outside the split or the pool, a row past the end of
          // the sequence: only in the block holding position L-1)
         uint32_t m0 = seg_ok ? mr2.x : mnone, m1 = seg_ok ? mr2.y : mnone;
-        const int blk = blk0 + kChunkBlocks * c + mblk;
+        const int blk = blk0 + kChunkBlocks * chunk_of(c) + mblk;
         if (blk == blk_hi || blk == blk_lo) {
           // my rows k with position p0 + k outside [qlo, qhi): k < nlo or k >= nhi
           const int p0 = blk * kBlockSize + mrow0;
@@ -1376,7 +1419,21 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
       pick_digits(sr, sr2, d0, d1, d2);
       float dg[kHeads];
       float dmax = -CUDART_INF_F;
-      if (kHeads == 1) {
+      // (kScore) positions from my token to the newest, and the score of my
+      // g-th head without the running max
+      const float dist = static_cast<float>(L - 1 - (blk0 * kBlockSize + kChunkTokens * chunk_of(c) + stok));
+      auto score_of = [&](int g) {
+        const int e12 = static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]);
+        const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[g]));
+        return scored(a, fmaf(mt.x, xg, mt.y * qs[g]), sm.slope[hb + g], dist);
+      };
+      if constexpr (kScore) {
+#pragma unroll
+        for (int g = 0; g < kHeads; ++g) {
+          dg[g] = score_of(g) - mr[g];
+          dmax = fmaxf(dmax, dg[g]);
+        }
+      } else if (kHeads == 1) {
         const int e12 = static_cast<int>(d1[0]) * 254 + static_cast<int>(d2[0]);
         const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[0]));
         dg[0] = fmaf(mt.x, xg, fmaf(mt.y, qs[0], -mr[0]));
@@ -1414,7 +1471,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
           const int gh = hb + g;
           const int e12 = static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]);
           const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[g]));
-          sg[g] = fmaf(mt.x, xg, mt.y * qs[g]);
+          sg[g] = kScore ? score_of(g) : fmaf(mt.x, xg, mt.y * qs[g]);
           float u = valid ? sg[g] + e : -CUDART_INF_F;
 #pragma unroll
           for (int o = 16; o; o >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
@@ -1572,17 +1629,19 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   if (take_ticket(a, b, h, &sm.is_last)) merge_records<G, kThreads>(a, b, h);
 }
 
-template <int G, int KB, int VB, bool kWide, bool kWin>
+template <int G, int KB, int VB, bool kWide, bool kWin, bool kScore>
 cudaError_t launch_gw(const DecodeArgs& a, cudaStream_t stream) {
   constexpr int kBytes = kSmemBytesOf<Fmt<KB, VB>::kSegBytes, kWide>;
-  const cudaError_t e = ensure_smem_limit<decode_kernel<G, KB, VB, kWide, kWin>>(kBytes);
+  const cudaError_t e = ensure_smem_limit<decode_kernel<G, KB, VB, kWide, kWin, kScore>>(kBytes);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.nsplit + (kWin ? 1 : 0), a.num_kv_heads, a.batch);  // (+ the window's CTA)
-  return launch_pdl(decode_kernel<G, KB, VB, kWide, kWin>, grid, dim3(Roles<kWide>::kThreads), kBytes, stream, a);
+  return launch_pdl(decode_kernel<G, KB, VB, kWide, kWin, kScore>, grid, dim3(Roles<kWide>::kThreads), kBytes, stream, a);
 }
 template <int G, int KB, int VB, bool kWide>
 cudaError_t launch_g(const DecodeArgs& a, cudaStream_t stream) {
-  return a.win != nullptr ? launch_gw<G, KB, VB, kWide, true>(a, stream) : launch_gw<G, KB, VB, kWide, false>(a, stream);
+  if (a.score) return launch_gw<G, KB, VB, kWide, false, true>(a, stream);
+  return a.win != nullptr ? launch_gw<G, KB, VB, kWide, true, false>(a, stream)
+                          : launch_gw<G, KB, VB, kWide, false, false>(a, stream);
 }
 
 template <int KB, int VB>
@@ -1640,8 +1699,8 @@ int decode_ctas_per_sm() {
   if (cached[dev] > 0) return cached[dev];
   int n = 0;
   constexpr int kBytes = kSmemBytesOf<Fmt<4, 2>::kSegBytes>;
-  if (ensure_smem_limit<decode_kernel<8, 4, 2, false, false>>(kBytes) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<8, 4, 2, false, false>, Roles<false>::kThreads, kBytes) !=
+  if (ensure_smem_limit<decode_kernel<8, 4, 2, false, false, false>>(kBytes) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<8, 4, 2, false, false, false>, Roles<false>::kThreads, kBytes) !=
           cudaSuccess ||
       n < 1)
     n = 1;

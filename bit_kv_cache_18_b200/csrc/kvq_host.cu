@@ -308,11 +308,26 @@ struct AppendRows {
   int64_t token_stride;
 };
 
+// Score options: KVQ_OK, or why they are refused.
+int check_score_opts(const kvq_score_opts* o) {
+  if (!std::isfinite(o->softmax_scale) || !std::isfinite(o->softcap) || o->softcap < 0.0f || o->window < 0)
+    return KVQ_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(o->alibi_slopes) % sizeof(float) != 0) return KVQ_ERR_INVALID;
+  return KVQ_OK;
+}
+
+// Tokens whose blocks a query with a sliding window can touch: the window may
+// start anywhere in a block.
+int32_t scored_span(int32_t max_seq_len, int32_t window) {
+  const int32_t longest = window > 0 && window < INT32_MAX - kBlockSize ? window + kBlockSize - 1 : INT32_MAX;
+  return max_seq_len < longest ? max_seq_len : longest;
+}
+
 int decode_impl(const kvq_cache_desc* desc, const void* q, kvq_dtype q_dtype, int32_t batch, int32_t num_q_heads,
                 const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* seq_lens,
                 int32_t max_seq_len, float softmax_scale, void* out, kvq_dtype out_dtype, void* workspace,
                 size_t ws_bytes, int32_t blocks_per_split, void* stream, const AppendRows* app,
-                const kvq_window_desc* win = nullptr) {
+                const kvq_window_desc* win = nullptr, const kvq_score_opts* opts = nullptr) {
   int rc = check_desc(desc);
   if (rc != KVQ_OK) return rc;
   if (batch < 0 || num_q_heads <= 0 || max_blocks_per_seq < 0 || max_seq_len < 0 ||
@@ -329,7 +344,8 @@ int decode_impl(const kvq_cache_desc* desc, const void* q, kvq_dtype q_dtype, in
   const bool use_win = win != nullptr && win->sink + win->recent > 0;
   if (use_win && batch > win->num_seqs) return KVQ_ERR_INVALID;
   DecodePlan plan;
-  rc = plan_decode(batch, desc->num_kv_heads, num_q_heads, max_seq_len, blocks_per_split, &plan, use_win ? 1 : 0);
+  const int32_t span = opts ? scored_span(max_seq_len, opts->window) : max_seq_len;
+  rc = plan_decode(batch, desc->num_kv_heads, num_q_heads, span, blocks_per_split, &plan, use_win ? 1 : 0);
   if (rc != KVQ_OK) return rc;
   if (!workspace || !aligned16(workspace) || ws_bytes < plan.total_bytes) return KVQ_ERR_WORKSPACE;
   if (!std::isfinite(softmax_scale)) return KVQ_ERR_INVALID;
@@ -364,6 +380,11 @@ int decode_impl(const kvq_cache_desc* desc, const void* q, kvq_dtype q_dtype, in
   a.win_sink = use_win ? win->sink : 0;
   a.win_recent = use_win ? win->recent : 0;
   a.nrec = plan.nrec;
+  a.score = opts ? 1 : 0;
+  a.softcap = opts ? opts->softcap * 1.4426950408889634074f : 0.0f;
+  a.softcap_exp = opts && opts->softcap > 0.0f ? 2.0f / opts->softcap : 0.0f;
+  a.score_window = opts ? opts->window : 0;
+  a.alibi_slopes = opts ? opts->alibi_slopes : nullptr;
   if (!a.status) return KVQ_ERR_CUDA;
   return launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
@@ -496,6 +517,145 @@ int kvq_decode_attention_noalloc(const kvq_cache_desc* desc, const void* q, kvq_
   return kvq_decode_attention_ex(desc, q, q_dtype, batch, num_q_heads, block_table, max_blocks_per_seq,
                                  seq_lens, max_seq_len, softmax_scale, out, out_dtype, scratch,
                                  kStaticScratchBytes, 0, stream);
+}
+
+size_t kvq_decode_scored_workspace_bytes(const kvq_cache_desc* desc, int32_t batch, int32_t num_q_heads,
+                                         int32_t max_seq_len, int32_t window) {
+  if (window < 0 || max_seq_len < 0) return 0;
+  return kvq_decode_workspace_bytes(desc, batch, num_q_heads, scored_span(max_seq_len, window));
+}
+
+int kvq_decode_attention_scored(const kvq_cache_desc* desc, const kvq_score_opts* opts, const void* q,
+                                kvq_dtype q_dtype, int32_t batch, int32_t num_q_heads, const int32_t* block_table,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len, void* out,
+                                kvq_dtype out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  const kvq_score_opts none = {};
+  if (!opts) opts = &none;
+  int rc = check_desc(desc);
+  if (rc == KVQ_OK) rc = check_score_opts(opts);
+  if (rc != KVQ_OK) return rc;
+  return decode_impl(desc, q, q_dtype, batch, num_q_heads, block_table, max_blocks_per_seq, seq_lens, max_seq_len,
+                     opts->softmax_scale, out, out_dtype, workspace, ws_bytes, 0, stream, nullptr, nullptr, opts);
+}
+
+int kvq_update_tables(int32_t* ring, int32_t capacity, const int32_t* state_in, int32_t* state_out,
+                      const int32_t* seq_lens, const int32_t* target_lens, int32_t* lens_out, int32_t batch,
+                      int32_t* block_table, int32_t max_blocks_per_seq, int32_t* cu_seqlens, int32_t max_tokens,
+                      int32_t* positions, int32_t* seq_ids, int32_t* slots, void* stream) {
+  if (capacity <= 0 || batch < 0 || max_blocks_per_seq < 0 || max_tokens < 0) return KVQ_ERR_INVALID;
+  if (batch > kMaxTableBatch) return KVQ_ERR_UNSUPPORTED;
+  if (!ring || !state_in || !state_out || !cu_seqlens) return KVQ_ERR_INVALID;
+  if (batch > 0 && (!seq_lens || !target_lens || !lens_out || (max_blocks_per_seq > 0 && !block_table)))
+    return KVQ_ERR_INVALID;
+  if (max_tokens > 0 && (!positions || !seq_ids || !slots)) return KVQ_ERR_INVALID;
+  TablesArgs a;
+  a.ring = ring;
+  a.capacity = capacity;
+  a.state_in = state_in;
+  a.state_out = state_out;
+  a.lens = seq_lens;
+  a.target = target_lens;
+  a.lens_out = lens_out;
+  a.batch = batch;
+  a.table = block_table;
+  a.max_blocks = max_blocks_per_seq;
+  a.cu_seqlens = cu_seqlens;
+  a.max_tokens = max_tokens;
+  a.positions = positions;
+  a.seq_ids = seq_ids;
+  a.slots = slots;
+  a.status = device_status_ptr();
+  if (!a.status) return KVQ_ERR_CUDA;
+  return launch_tables(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+namespace {
+int check_rope_desc(const kvq_rope_desc* d) {
+  if (!d || (d->interleaved != 0 && d->interleaved != 1) || d->scaling < KVQ_ROPE_NONE || d->scaling > KVQ_ROPE_YARN)
+    return KVQ_ERR_INVALID;
+  if (!std::isfinite(d->base) || d->base <= 1.0) return KVQ_ERR_INVALID;
+  if (d->scaling != KVQ_ROPE_NONE && !(std::isfinite(d->factor) && d->factor >= 1.0)) return KVQ_ERR_INVALID;
+  if ((d->scaling == KVQ_ROPE_BANDS || d->scaling == KVQ_ROPE_YARN) &&
+      !(d->original_len > 0 && d->low > 0.0 && d->high > d->low && std::isfinite(d->high)))
+    return KVQ_ERR_INVALID;
+  if (d->rotary_dim < 16 || d->rotary_dim > kHeadDim || d->rotary_dim % 16 != 0) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+}  // namespace
+
+int kvq_rope_table(const kvq_rope_desc* desc, uint64_t* turns_out, float* magnitude_out) {
+  const int rc = check_rope_desc(desc);
+  if (rc != KVQ_OK) return rc;
+  if (!turns_out || !magnitude_out) return KVQ_ERR_INVALID;
+  const long double two_pi = 6.283185307179586476925286766559L;
+  const long double dim = desc->rotary_dim, factor = desc->factor, len = desc->original_len;
+  long double base = desc->base, lo = 0.0L, hi = 0.0L;
+  if (desc->scaling == KVQ_ROPE_NTK) base *= powl(factor, dim / (dim - 2.0L));
+  if (desc->scaling == KVQ_ROPE_YARN) {
+    auto index = [&](long double turns) { return dim * logl(len / (turns * two_pi)) / (2.0L * logl(base)); };
+    lo = std::max(floorl(index(desc->high)), 0.0L);
+    hi = std::min(ceill(index(desc->low)), dim - 1.0L);
+  }
+  for (int i = 0; i < desc->rotary_dim / 2; ++i) {
+    long double f = powl(base, -2.0L * i / dim);
+    if (desc->scaling == KVQ_ROPE_LINEAR) {
+      f /= factor;
+    } else if (desc->scaling == KVQ_ROPE_BANDS) {
+      const long double k = (len * f / two_pi - desc->low) / (static_cast<long double>(desc->high) - desc->low);
+      const long double keep = std::min(std::max(k, 0.0L), 1.0L);
+      f = keep * f + (1.0L - keep) * f / factor;
+    } else if (desc->scaling == KVQ_ROPE_YARN) {
+      const long double d = std::min(std::max((i - lo) / std::max(hi - lo, 0.001L), 0.0L), 1.0L);
+      f = d * f / factor + (1.0L - d) * f;
+    }
+    const long double t = f / two_pi;  // < 1/6 turn a position
+    turns_out[i] = static_cast<uint64_t>(ldexpl(t, 64));
+  }
+  *magnitude_out = desc->scaling == KVQ_ROPE_YARN ? static_cast<float>(0.1L * logl(factor) + 1.0L) : 1.0f;
+  return KVQ_OK;
+}
+
+int kvq_rope(const kvq_rope_desc* desc, const uint64_t* turns, float magnitude, const int32_t* positions,
+             int32_t n_tokens, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+             int32_t num_q_heads, const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
+             int32_t num_k_heads, kvq_dtype dtype, void* stream) {
+  const int rc = check_rope_desc(desc);
+  if (rc != KVQ_OK) return rc;
+  if (n_tokens < 0 || num_q_heads < 0 || num_k_heads < 0 || num_q_heads > kMaxRopeHeads ||
+      num_k_heads > kMaxRopeHeads || !std::isfinite(magnitude))
+    return KVQ_ERR_INVALID;
+  if (dtype != KVQ_F16 && dtype != KVQ_BF16) return dtype == KVQ_F32 ? KVQ_ERR_UNSUPPORTED : KVQ_ERR_INVALID;
+  if (n_tokens == 0 || num_q_heads + num_k_heads == 0) return KVQ_OK;
+  if (!turns || !positions || reinterpret_cast<uintptr_t>(turns) % 8 != 0) return KVQ_ERR_INVALID;
+  auto bad_rows = [&](const void* p, int64_t stride, int32_t heads) {
+    return heads > 0 && (!p || !aligned16(p) || stride < static_cast<int64_t>(heads) * kHeadDim || stride % 8 != 0);
+  };
+  if (bad_rows(q, q_stride, num_q_heads) || bad_rows(q_out, q_out_stride, num_q_heads) ||
+      bad_rows(k, k_stride, num_k_heads) || bad_rows(k_out, k_out_stride, num_k_heads))
+    return KVQ_ERR_INVALID;
+  // in place only row by row
+  if ((num_q_heads > 0 && q == q_out && q_stride != q_out_stride) ||
+      (num_k_heads > 0 && k == k_out && k_stride != k_out_stride))
+    return KVQ_ERR_INVALID;
+  RopeArgs a;
+  a.turns = turns;
+  a.magnitude = magnitude;
+  a.rotary_dim = desc->rotary_dim;
+  a.interleaved = desc->interleaved;
+  a.bf16 = dtype == KVQ_BF16 ? 1 : 0;
+  a.positions = positions;
+  a.n_tokens = n_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_k_heads = num_k_heads;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.k = static_cast<const uint16_t*>(k);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.k_stride = k_stride;
+  a.k_out_stride = k_out_stride;
+  return launch_rope(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 int kvq_selftest_wait_timeout(uint32_t limit_us, uint64_t* elapsed_ns, void* stream) {

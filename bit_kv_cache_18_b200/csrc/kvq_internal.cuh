@@ -272,6 +272,13 @@ struct DecodeArgs {
   const uint16_t* win;  // nullptr: no window (nrec = nsplit)
   int32_t win_sink, win_recent;
   int32_t nrec;  // records per (b, query head) in partials
+  // optional score options (kvq_score_opts); never together with an append or
+  // a bf16 window
+  int32_t score;              // 0: none of the fields below is read
+  float softcap;              // cap log2(e); 0: no cap
+  float softcap_exp;          // e^(2 s / cap) = 2^(softcap_exp x base-2 score)
+  int32_t score_window;       // positions a query reads; 0: all
+  const float* alibi_slopes;  // [num_q_heads] or nullptr
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 
@@ -290,6 +297,47 @@ struct WindowAppendArgs {
 cudaError_t launch_window_append(const WindowAppendArgs& a, cudaStream_t stream);
 constexpr int kMaxWindowSink = 64;
 constexpr int kMaxWindowRecent = 1024;
+
+// Step tables (kvq_update_tables).
+struct TablesArgs {
+  int32_t* ring;
+  int32_t capacity;
+  const int32_t* state_in;
+  int32_t* state_out;
+  const int32_t* lens;
+  const int32_t* target;
+  int32_t* lens_out;
+  int32_t batch;
+  int32_t* table;
+  int32_t max_blocks;
+  int32_t* cu_seqlens;
+  int32_t max_tokens;
+  int32_t* positions;
+  int32_t* seq_ids;
+  int32_t* slots;
+  int* status;
+};
+cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
+constexpr int kMaxTableBatch = 16384;
+
+// Rotary positions (kvq_rope).
+struct RopeArgs {
+  const uint64_t* turns;  // [rotary_dim / 2]: turns per position, in units of 2^-64
+  float magnitude;
+  int32_t rotary_dim, interleaved, bf16;
+  const int32_t* positions;
+  int32_t n_tokens;
+  // the heads of both tensors; strides in elements
+  int32_t num_q_heads, num_k_heads;
+  const uint16_t* q;
+  uint16_t* q_out;
+  int64_t q_stride, q_out_stride;
+  const uint16_t* k;
+  uint16_t* k_out;
+  int64_t k_stride, k_out_stride;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
+constexpr int kMaxRopeHeads = 65536;
 
 // Failure-detection self-test (kvq_selftest_wait_timeout) and the time after
 // which a kernel's bounded wait gives up.

@@ -324,6 +324,135 @@ int kvq_decode_attention_window(const kvq_cache_desc* desc, const kvq_window_des
                                 const int32_t* seq_lens, int32_t max_seq_len, float softmax_scale, void* out,
                                 kvq_dtype out_dtype, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- a serving step around the cache ------------------------------------
+ * The pages' backend is a plugin of a serving engine ("Трюк Huawei с
+ * KV-кэшем" (beyondheadline.xyz), lede; "KVarN vs TurboQuant" (dothoosh.com),
+ * flag paragraph): a step gives its tokens places in the cache, rotates their
+ * queries and keys, writes them (kvq_quantize_append, kvq_window_append) and
+ * attends -- a prompt over its own rows, a running request's token over the
+ * packed cache.  The entry points below are the parts of that step which the
+ * two paths above leave out; the pages give no definition of them, so each is
+ * defined here. */
+
+/* Step tables, on the GPU.  Free blocks lie in a ring: `ring` holds
+ * `capacity` block ids (each >= 0, at most 2^27 - 2), of which
+ * state[1] starting at index state[0] (wrapping) are free, in the order in
+ * which they are handed out.  state is four int32 words: head, count, a
+ * ticket (zero before the first call; every call leaves it zero) and one
+ * reserved.  With all blocks of a pool either free or held by one sequence
+ * and capacity >= their number, the ring never overflows.
+ *
+ * seq_lens[b] is the present length of sequence b, target_lens[b] the one it
+ * is to have; with have = ceil(seq_lens[b]/16), want = ceil(target_lens[b]/16):
+ *   - a growing sequence takes want - have blocks from the head of the ring,
+ *     in batch order, into entries have .. want-1 of its block_table row, and
+ *     gets one new token per position seq_lens[b] .. target_lens[b]-1;
+ *   - a shrinking one (0: finished) returns blocks want .. have-1 to the tail
+ *     of the ring, in batch order; they can be taken from the next call on,
+ *     and its row is left as it was;
+ *   - in batch order, the first growing sequence for which the free blocks or
+ *     max_tokens do not suffice, and every growing one after it, is left as
+ *     it was (KVQ_ERR_POOL_EXHAUSTED or KVQ_ERR_OUT_OF_RANGE is recorded in
+ *     the device status word); so is a sequence one of whose lengths is
+ *     outside [0, 16*max_blocks_per_seq] (KVQ_ERR_OUT_OF_RANGE).
+ * lens_out[b] is the length that sequence b now has; cu_seqlens [batch+1]
+ * the running sum of the new tokens per sequence (the packed batch of
+ * kvq_prefill_attention); for packed token n, positions[n], seq_ids[n] and
+ * slots[n] (as in kvq_quantize_append and kvq_window_append), and -1 in all
+ * three from cu_seqlens[batch] to max_tokens, so that fixed-size buffers can
+ * be used with captured graphs.  state_out gets the new head and count.
+ * lens_out may be seq_lens and state_out may be state_in; otherwise no two
+ * buffers may overlap.  All pointers are device memory; batch <= 16384.  A
+ * state outside the ring is recorded as KVQ_ERR_OUT_OF_RANGE; no block is
+ * then taken or returned.  Block ids are passed on as they are: a negative
+ * or too large one gives slot -1, recorded.  One launch, asynchronous on the
+ * stream; calls on one state must be ordered. */
+int kvq_update_tables(int32_t* ring, int32_t capacity, const int32_t* state_in, int32_t* state_out,
+                      const int32_t* seq_lens, const int32_t* target_lens, int32_t* lens_out, int32_t batch,
+                      int32_t* block_table, int32_t max_blocks_per_seq, int32_t* cu_seqlens, int32_t max_tokens,
+                      int32_t* positions, int32_t* seq_ids, int32_t* slots, void* stream);
+
+/* Rotary positions.  Pair i of a head vector x, i < rotary_dim/2, is
+ * (x[2i], x[2i+1]) with `interleaved` set, else (x[i], x[i + rotary_dim/2]);
+ * at position p it becomes
+ *   magnitude * (a cos(p f_i) - b sin(p f_i), b cos(p f_i) + a sin(p f_i)),
+ * and x[rotary_dim ..] stays as it is.  With g_i = base^(-2i/rotary_dim):
+ *   KVQ_ROPE_NONE    f_i = g_i
+ *   KVQ_ROPE_LINEAR  f_i = g_i / factor
+ *   KVQ_ROPE_NTK     f_i = g_i for the base base*factor^(rotary_dim/(rotary_dim-2))
+ *   KVQ_ROPE_BANDS   f_i = k g_i + (1-k) g_i/factor, k the turns that pair i
+ *                    makes over original_len, (original_len g_i/2pi - low) /
+ *                    (high - low), cut to [0, 1]
+ *   KVQ_ROPE_YARN    f_i = d g_i/factor + (1-d) g_i, d = (i - lo)/(hi - lo)
+ *                    cut to [0, 1], lo = max(floor(I(high)), 0), hi =
+ *                    min(ceil(I(low)), rotary_dim - 1), I(n) = rotary_dim
+ *                    ln(original_len/(2pi n)) / (2 ln base), hi - lo at least
+ *                    0.001; magnitude = 0.1 ln(factor) + 1
+ * magnitude is 1 but for KVQ_ROPE_YARN. */
+typedef enum {
+  KVQ_ROPE_NONE = 0,
+  KVQ_ROPE_LINEAR = 1,
+  KVQ_ROPE_NTK = 2,
+  KVQ_ROPE_BANDS = 3,
+  KVQ_ROPE_YARN = 4
+} kvq_rope_scaling;
+typedef struct {
+  int32_t rotary_dim;   /* a multiple of 16 in [16, 128]                       */
+  int32_t interleaved;  /* 0: half layout, 1: interleaved pairs                */
+  int32_t scaling;      /* kvq_rope_scaling                                    */
+  int32_t original_len; /* BANDS, YARN: length the model was trained on, > 0   */
+  double base;          /* > 1                                                 */
+  double factor;        /* >= 1 (all but NONE)                                 */
+  double low, high;     /* BANDS, YARN: numbers of turns, 0 < low < high       */
+} kvq_rope_desc;
+
+/* The table kvq_rope reads: turns_out[i] = f_i/2pi modulo 1 in units of
+ * 2^-64 (host memory, rotary_dim/2 entries), and the magnitude.  Host only.
+ * KVQ_ERR_UNSUPPORTED for a rotary_dim the kernel does not cover,
+ * KVQ_ERR_INVALID for other values out of range. */
+int kvq_rope_table(const kvq_rope_desc* desc, uint64_t* turns_out, float* magnitude_out);
+
+/* Rotate the queries and keys of n_tokens tokens, one launch.  q: device,
+ * row t at element t*q_stride, [num_q_heads, 128] of dtype (F16 or BF16);
+ * q_out the same with its own stride, and either q itself with the same
+ * stride (in place) or memory that does not overlap it; k and k_out likewise
+ * with num_k_heads.  A tensor with 0 heads is not read (its pointers may be
+ * NULL).  16-byte aligned pointers, strides >= heads*128 and multiples of 8.
+ * turns: the device copy of kvq_rope_table's table for the same desc;
+ * positions: device int32 [n_tokens]; the rows of a token with a negative
+ * position (padding) are neither read nor written.  Angles are exact to 2^-32
+ * of a turn at every position, the arithmetic is fp32, rounded once. */
+int kvq_rope(const kvq_rope_desc* desc, const uint64_t* turns, float magnitude, const int32_t* positions,
+             int32_t n_tokens, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+             int32_t num_q_heads, const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
+             int32_t num_k_heads, kvq_dtype dtype, void* stream);
+
+/* Scores of models whose attention is not a plain softmax of scaled products.
+ * For a query at position t and a key at position j, head h:
+ *   s = tau q.k;  softcap > 0: s = softcap tanh(s/softcap);
+ *   alibi_slopes: s -= alibi_slopes[h] |t - j|;
+ *   window > 0: keys with t - j >= window are not read.
+ * Zero and NULL switch an option off; a NULL kvq_score_opts is all off. */
+typedef struct {
+  float softmax_scale;       /* tau; <= 0: 1/sqrt(128)                          */
+  float softcap;             /* >= 0                                            */
+  int32_t window;            /* >= 0                                            */
+  const float* alibi_slopes; /* device fp32 [num_q_heads], finite, or NULL      */
+} kvq_score_opts;
+
+/* kvq_decode_attention with score options: the query of sequence b stands at
+ * position seq_lens[b] - 1.  Blocks that lie wholly before the window are not
+ * read (their block_table entries may name blocks given back).  Arguments,
+ * status rules and workspace rules are those of kvq_decode_attention; the
+ * workspace size is that of kvq_decode_scored_workspace_bytes, which needs
+ * the window that the call will use. */
+size_t kvq_decode_scored_workspace_bytes(const kvq_cache_desc* desc, int32_t batch, int32_t num_q_heads,
+                                         int32_t max_seq_len, int32_t window);
+int kvq_decode_attention_scored(const kvq_cache_desc* desc, const kvq_score_opts* opts, const void* q,
+                                kvq_dtype q_dtype, int32_t batch, int32_t num_q_heads, const int32_t* block_table,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len, void* out,
+                                kvq_dtype out_dtype, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise the stream, then read and clear the current device's status
  * word: KVQ_OK, or the first error that a kernel recorded since the last
  * read (KVQ_ERR_OUT_OF_RANGE, KVQ_ERR_DEVICE_TIMEOUT).  Returns
