@@ -104,6 +104,8 @@ def lib():
                 "kvq_rope_table": (ctypes.c_int, [ctypes.POINTER(RopeDesc), vp, vp]),
                 "kvq_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), vp, f32, vp, i32, vp, i64, vp, i64, i32, vp,
                                             i64, vp, i64, i32, ctypes.c_int, vp]),
+                "kvq_prefill_attention": (ctypes.c_int, [ctypes.POINTER(ScoreOpts), vp, i64, vp, i64, vp, i64, vp, i64,
+                                                         i32, i32, i32, vp, i32, vp, ctypes.c_int, vp]),
                 "kvq_decode_scored_workspace_bytes": (sz, [dp, i32, i32, i32, i32]),
                 "kvq_decode_attention_scored": (ctypes.c_int, [dp, ctypes.POINTER(ScoreOpts), vp, ctypes.c_int, i32,
                                                                i32, vp, i32, vp, i32, vp, ctypes.c_int, vp, sz, vp]),
@@ -446,6 +448,28 @@ def _require_opts(what: str, opts, num_q_heads: int):
     slopes = getattr(opts, "slopes_tensor", None)
     _require_on_device(what, slopes)
     _require(slopes is None or slopes.numel() == num_q_heads, f"{what}: one slope per query head")
+
+
+def kvq_prefill_attention(q, k, v, cu_seqlens, out, opts=None, prefix_lens=None, stream=None):
+    """Attention of whole prompts over their own rows: q and out [n, Hq, 128],
+    k and v [n, Hkv, 128] (fp16 or bf16; slices of a fused projection do),
+    cu_seqlens int32 [batch + 1], prefix_lens int32 [batch] or None, opts from
+    make_score_opts."""
+    what = "kvq_prefill_attention"
+    batch = cu_seqlens.numel() - 1
+    _require_on_device(what, q, k, v, out, cu_seqlens, prefix_lens)
+    _require_int32(what, cu_seqlens, prefix_lens)
+    _require_rows(what, q, k, v, out)
+    _require(batch >= 0 and out.shape == q.shape and k.shape == v.shape and k.shape[0] == q.shape[0] and
+             q.dtype == k.dtype == v.dtype == out.dtype and (prefix_lens is None or prefix_lens.numel() == batch),
+             f"{what}: shapes and types")
+    if opts is not None:
+        _require_opts(what, opts, q.shape[1])
+    rc = lib().kvq_prefill_attention(ctypes.byref(opts) if opts is not None else None, _ptr(q), _row_stride(q),
+                                     _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(out), _row_stride(out),
+                                     q.shape[0], q.shape[1], k.shape[1], _ptr(cu_seqlens), batch, _ptr(prefix_lens),
+                                     _dtype_code(q), _stream_ptr(stream))
+    _check(rc, what)
 
 
 def kvq_decode_scored_workspace_bytes(num_blocks, num_kv_heads, batch, num_q_heads, max_seq_len, window=0,

@@ -538,6 +538,57 @@ int kvq_decode_attention_scored(const kvq_cache_desc* desc, const kvq_score_opts
                      opts->softmax_scale, out, out_dtype, workspace, ws_bytes, 0, stream, nullptr, nullptr, opts);
 }
 
+int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, void* out, int64_t out_stride,
+                          int32_t n_tokens, int32_t num_q_heads, int32_t num_kv_heads, const int32_t* cu_seqlens,
+                          int32_t batch, const int32_t* prefix_lens, kvq_dtype dtype, void* stream) {
+  const kvq_score_opts none = {};
+  if (!opts) opts = &none;
+  const int rc = check_score_opts(opts);
+  if (rc != KVQ_OK) return rc;
+  if (n_tokens < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0) return KVQ_ERR_INVALID;
+  if (dtype != KVQ_F16 && dtype != KVQ_BF16) return dtype == KVQ_F32 ? KVQ_ERR_UNSUPPORTED : KVQ_ERR_INVALID;
+  const int32_t group = num_q_heads % num_kv_heads == 0 ? num_q_heads / num_kv_heads : 0;
+  if (group != 1 && group != 2 && group != 4 && group != 8) return KVQ_ERR_UNSUPPORTED;
+  if (num_q_heads > kMaxRopeHeads) return KVQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0 || batch == 0) return KVQ_OK;
+  if (!cu_seqlens) return KVQ_ERR_INVALID;
+  auto bad_rows = [&](const void* p, int64_t stride, int32_t heads) {
+    return !p || !aligned16(p) || stride < static_cast<int64_t>(heads) * kHeadDim || stride % 8 != 0 ||
+           stride >= (int64_t{1} << 38);
+  };
+  if (bad_rows(q, q_stride, num_q_heads) || bad_rows(k, k_stride, num_kv_heads) || bad_rows(v, v_stride, num_kv_heads) ||
+      bad_rows(out, out_stride, num_q_heads) || out == q || out == k || out == v)
+    return KVQ_ERR_INVALID;
+  PrefillArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.out = static_cast<uint16_t*>(out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.out_stride = out_stride;
+  a.bf16 = dtype == KVQ_BF16 ? 1 : 0;
+  a.log_group = group == 8 ? 3 : group == 4 ? 2 : group == 2 ? 1 : 0;
+  a.num_kv_heads = num_kv_heads;
+  a.n_tokens = n_tokens;
+  a.cu_seqlens = cu_seqlens;
+  a.batch = batch;
+  a.prefix_lens = prefix_lens;
+  const float tau = opts->softmax_scale > 0.0f ? opts->softmax_scale : 0.08838834764831844055f;
+  a.scale_log2 = tau * 1.4426950408889634074f;
+  a.softcap = opts->softcap * 1.4426950408889634074f;
+  a.softcap_exp = opts->softcap > 0.0f ? 2.0f * a.scale_log2 / opts->softcap : 0.0f;
+  a.window = opts->window;
+  a.alibi_slopes = opts->alibi_slopes;
+  a.status = device_status_ptr();
+  if (!a.status) return KVQ_ERR_CUDA;
+  const int64_t ctas = ((static_cast<int64_t>(n_tokens) * group / 256) + batch) * num_kv_heads;
+  if (ctas > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  return launch_prefill(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
 int kvq_update_tables(int32_t* ring, int32_t capacity, const int32_t* state_in, int32_t* state_out,
                       const int32_t* seq_lens, const int32_t* target_lens, int32_t* lens_out, int32_t batch,
                       int32_t* block_table, int32_t max_blocks_per_seq, int32_t* cu_seqlens, int32_t max_tokens,

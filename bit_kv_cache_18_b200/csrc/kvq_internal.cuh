@@ -5,6 +5,7 @@
 // launcher entry points that kvq_host.cu calls.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -338,6 +339,30 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 constexpr int kMaxRopeHeads = 65536;
+
+// Attention of whole prompts (kvq_prefill_attention).
+struct PrefillArgs {
+  CUtensorMap map_q, map_k, map_v;  // filled by launch_prefill
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;
+  int64_t q_stride, k_stride, v_stride, out_stride;  // elements from one token's row to the next
+  int32_t bf16;
+  int32_t log_group;  // log2(query heads per kv head)
+  int32_t num_kv_heads;
+  int32_t n_tokens;
+  const int32_t* cu_seqlens;
+  int32_t batch;
+  const int32_t* prefix_lens;  // or nullptr
+  float scale_log2;            // softmax scale times log2(e)
+  // score options as in DecodeArgs, but softcap_exp takes the raw product q.k
+  float softcap, softcap_exp;
+  int32_t window;
+  const float* alibi_slopes;
+  int* status;
+};
+cudaError_t launch_prefill(PrefillArgs& a, cudaStream_t stream);
 
 // Failure-detection self-test (kvq_selftest_wait_timeout) and the time after
 // which a kernel's bounded wait gives up.

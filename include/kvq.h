@@ -440,6 +440,28 @@ typedef struct {
   const float* alibi_slopes; /* device fp32 [num_q_heads], finite, or NULL      */
 } kvq_score_opts;
 
+/* Attention of whole prompts over their own rows.  batch prompts lie one after
+ * the other in the rows of q, k, v and out: prompt b in rows cu_seqlens[b] ..
+ * cu_seqlens[b+1]-1 (device int32 [batch+1], ascending, within [0, n_tokens]; a
+ * prompt whose bounds are not is left out and recorded as
+ * KVQ_ERR_OUT_OF_RANGE; prompts may be empty).  Row t of a tensor starts at
+ * element t*stride: [num_q_heads, 128] for q and out, [num_kv_heads, 128] for
+ * k and v, all of dtype (F16 or BF16).  The query at position t of a prompt of
+ * n tokens reads the keys j with
+ *   (j <= t or j < prefix_lens[b]) and (window == 0 or t - j < window),
+ * scores as above, and gets sum_j softmax(s)_j v_j, rounded to dtype.
+ * prefix_lens: device int32 [batch] (cut to [0, n]) or NULL for none.  The
+ * rows that belong to no prompt are not written, and what stands in keys and
+ * values that a query does not read (infinities and NaN too) does not reach
+ * its output.  num_q_heads / num_kv_heads is 1, 2, 4 or 8; pointers 16-byte
+ * aligned, strides >= heads*128 and multiples of 8; out must not overlap the
+ * inputs.  The products' sums, the softmax and its sums are fp32, the
+ * probabilities enter the second product in dtype.  One launch, no workspace. */
+int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, void* out, int64_t out_stride,
+                          int32_t n_tokens, int32_t num_q_heads, int32_t num_kv_heads, const int32_t* cu_seqlens,
+                          int32_t batch, const int32_t* prefix_lens, kvq_dtype dtype, void* stream);
+
 /* kvq_decode_attention with score options: the query of sequence b stands at
  * position seq_lens[b] - 1.  Blocks that lie wholly before the window are not
  * read (their block_table entries may name blocks given back).  Arguments,

@@ -1,0 +1,301 @@
+"""kvq_prefill_attention against its definition in 64 bits.
+
+Tolerance of an output o = sum p v / sum p, with A = sum p |v| / sum p:
+  - eps/2 of |o|: the output's rounding; eps/2 of A: that of each p;
+  - 2 e A for a score error e on both sums: the fp32 accumulation of 128
+    products over up to 128 additions of at most a step each, 2^-23 * 2^4 (the
+    sums inside a product are wider than their sequence) of sum |q k| tau, the
+    softcap's 2^-21 cap, the distance bias's 2^-23 of it, exponentials 2^-21;
+  - fp16: a p below 2^-14 is rounded to 2^-25, l is at least 1: n 2^-25 max |v|.
+"""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _t(name):
+    import torch
+    return {"bf16": torch.bfloat16, "fp16": torch.float16}[name]
+
+
+def _reference(q, k, v, lens, starts, prefixes, scale=0.0, softcap=0.0, window=0, slopes=None):
+    """-> outputs in 64 bits (rows of no prompt NaN), tolerance."""
+    import torch
+    G = q.shape[1] // k.shape[1]
+    tau = scale if scale > 0 else 1 / math.sqrt(128)
+    eps = torch.finfo(q.dtype).eps
+    out = torch.full(q.shape, float("nan"), dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(out)
+    for n, s0, pre in zip(lens, starts, prefixes):
+        if n == 0:
+            continue
+        for h in range(q.shape[1]):
+            qq, kk, vv = (x.double() for x in (q[s0:s0 + n, h], k[s0:s0 + n, h // G], v[s0:s0 + n, h // G]))
+            t, j = torch.arange(n, device="cuda")[:, None], torch.arange(n, device="cuda")[None, :]
+            ok = (j <= t) | (j < pre)
+            if window:
+                ok &= t - j < window
+            s = qq @ kk.nan_to_num(0, 0, 0).T * tau
+            size = (qq.abs() @ kk.nan_to_num(0, 0, 0).abs().T * tau).masked_fill(~ok, 0).amax(1, keepdim=True)
+            if softcap:
+                s = softcap * torch.tanh(s / softcap)
+            bias = 0.0
+            if slopes is not None:
+                bias = float(slopes[h]) * (t - j).abs().double()
+                s = s - bias
+                bias = bias.masked_fill(~ok, 0).amax(1, keepdim=True)
+            p = torch.softmax(s.masked_fill(~ok, -math.inf), 1)
+            vz = vv.nan_to_num(0, 0, 0)
+            out[s0:s0 + n, h] = p @ vz
+            A = p @ vz.abs()
+            e = 2.0 ** -19 * size + 2.0 ** -21 * (1 + softcap) + 2.0 ** -23 * bias
+            x = (eps / 2) * (out[s0:s0 + n, h].abs() + A) + 2 * e * A + 1e-30
+            if q.dtype == torch.float16:
+                x = x + 2.0 ** -24 + n * 2.0 ** -25 * vz.abs().amax()
+            tol[s0:s0 + n, h] = x
+    return out, tol
+
+
+def _rows(n, heads, dtype, g, mul=1.0):
+    import torch
+    x = torch.randn(n, heads, 128, device="cuda", generator=g)
+    x[..., ::41] *= mul
+    return x.to(_t(dtype))
+
+
+def _run(kvq, lens, hq, hkv, dtype="bf16", prefixes=None, pad=0, seed=0, mutate=None, **opts):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1000 + seed)
+    n = sum(lens) + pad
+    q, k, v = _rows(n, hq, dtype, g), _rows(n, hkv, dtype, g, 15.0), _rows(n, hkv, dtype, g)
+    if mutate:
+        mutate(q, k, v)
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    slopes = opts.get("alibi_slopes")
+    dev = dict(opts, alibi_slopes=None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device="cuda"))
+    out = torch.full_like(q, 7.0)
+    kvq.kvq_prefill_attention(q, k, v, torch.from_numpy(starts).cuda(), out, opts=kvq.make_score_opts(**dev),
+                              prefix_lens=None if prefixes is None else
+                              torch.tensor(prefixes, dtype=torch.int32, device="cuda"))
+    assert kvq.kvq_last_device_status() == 0
+    want, tol = _reference(q, k, v, lens, starts, prefixes or [0] * len(lens), opts.get("softmax_scale", 0.0),
+                           opts.get("softcap", 0.0), opts.get("window", 0),
+                           None if slopes is None else np.float32(slopes))
+    _close(out[:sum(lens)], want[:sum(lens)], tol[:sum(lens)])
+    assert (out[sum(lens):] == 7.0).all()  # rows behind the last prompt
+    return out
+
+
+def _close(out, want, tol):
+    import torch
+    err = (out.double() - want).abs()
+    assert torch.isfinite(out).all(), (~torch.isfinite(out)).nonzero()[:4]
+    worst = (err - tol).argmax()
+    assert (err <= tol).all(), (float(err.flatten()[worst]), float(tol.flatten()[worst]), np.unravel_index(
+        int(worst), tuple(out.shape)))
+
+
+def _slopes(n):
+    return [2.0 ** (-8.0 * (h + 1) / n) for h in range(n)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [1, 2, 4, 8])
+@pytest.mark.parametrize("lens", [[1], [20], [128], [129], [257], [700]], ids=str)
+def test_one_prompt(kvq, cuda, group, lens, dtype):
+    _run(kvq, lens, 2 * group, 2, dtype, seed=group)
+
+
+@pytest.mark.parametrize("opts", [
+    {}, dict(softcap=50.0), dict(softcap=5.0), dict(window=1), dict(window=2), dict(window=128), dict(window=129),
+    dict(window=300), dict(alibi_slopes=_slopes(8)), dict(softcap=30.0, window=77, alibi_slopes=_slopes(8)),
+    dict(softmax_scale=0.03, softcap=20.0)], ids=lambda o: "-".join(f"{k}{v if k == 'window' else ''}" for k, v in
+                                                                   o.items()) or "none")
+@pytest.mark.parametrize("hkv", [1, 8])
+@pytest.mark.parametrize("prefix", [False, True])
+def test_options_ragged(kvq, cuda, opts, hkv, prefix):
+    lens = [17, 0, 500, 1, 128, 333, 0, 64, 1025]
+    _run(kvq, lens, 8, hkv, "fp16" if prefix else "bf16", prefixes=[n // 3 if i % 3 else n for i, n in enumerate(lens)]
+         if prefix else None, pad=13, seed=hkv, **opts)
+
+
+@pytest.mark.parametrize("prefixes", [[0, 5000], [-3, 1], [300, 299], [2 ** 31 - 1, 150]])
+def test_prefix_bounds(kvq, cuda, prefixes):
+    """Cut to the prompt; negative ones are none."""
+    import torch
+    lens = [300, 300]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (_rows(600, 2, "bf16", g) for _ in range(3))
+    out = torch.empty_like(q)
+    kvq.kvq_prefill_attention(q, k, v, torch.tensor([0, 300, 600], dtype=torch.int32, device="cuda"), out,
+                              prefix_lens=torch.tensor(prefixes, dtype=torch.int32, device="cuda"))
+    want, tol = _reference(q, k, v, lens, [0, 300], prefixes)
+    _close(out, want, tol)
+
+
+def test_many_short_prompts(kvq, cuda):
+    """More prompts than threads; the order of the items over them."""
+    rng = np.random.default_rng(3)
+    _run(kvq, [int(x) for x in rng.integers(0, 9, 900)], 4, 2, "bf16")
+
+
+@pytest.mark.parametrize("group", [1, 8])
+def test_long_prompt(kvq, cuda, group):
+    _run(kvq, [5000], group, 1, "bf16", seed=9)
+
+
+def test_large_scores_and_saturated_caps(kvq, cuda):
+    """Scores of hundreds: the running max moves in most tiles; then the same under a small and a huge cap."""
+    def louder(q, k, v):
+        q.mul_(30)
+    _run(kvq, [600, 40], 4, 2, "bf16", mutate=louder)
+    _run(kvq, [600, 40], 4, 2, "bf16", mutate=louder, softcap=2.0)
+    _run(kvq, [600, 40], 4, 2, "bf16", softcap=3e5)
+
+
+def test_rising_scores_move_the_maximum(kvq, cuda):
+    """Keys of one direction whose length falls with the position: the oldest tile has the largest scores."""
+    import torch
+
+    def rising(q, k, v):
+        n = k.shape[0]
+        q.copy_(torch.ones_like(q))
+        k.copy_((torch.linspace(12, 0.1, n, device="cuda")[:, None, None] * torch.ones_like(k.float())).to(k.dtype))
+    _run(kvq, [900], 2, 1, "bf16", mutate=rising)
+    _run(kvq, [900], 2, 1, "fp16", mutate=rising)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("group", [1, 4])
+def test_masked_places_do_not_reach_a_row(kvq, cuda, bad, group):
+    """NaN and infinities in later tokens' keys and values, in rows behind the last prompt and before the window:
+    every row that does not read them is as without them."""
+    import torch
+    lens, pad = [300, 70], 40
+
+    def spoil(q, k, v):
+        v[250, :, 3] = bad
+        k[250, :, 100] = bad
+        v[370:] = bad
+        k[370:] = bad
+        q[370:] = bad
+    starts = [0, 300]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q, k, v = _rows(410, 2 * group, "bf16", g), _rows(410, 2, "bf16", g), _rows(410, 2, "bf16", g)
+    spoil(q, k, v)
+    cu = torch.tensor([0, 300, 370], dtype=torch.int32, device="cuda")
+    for window in (0, 20):
+        out = torch.full_like(q, 7.0)
+        kvq.kvq_prefill_attention(q, k, v, cu, out, opts=kvq.make_score_opts(window=window))
+        want, tol = _reference(q, k, v, lens, starts, [0, 0], window=window)
+        for rows in (slice(0, 250), slice(300, 370)) + ((slice(270, 300),) if window else ()):
+            _close(out[rows], want[rows], tol[rows])
+        assert (out[370:] == 7.0).all()
+        assert not torch.isfinite(out[250:250 + (window or 50)]).all(-1).any()  # those that read them
+    # a value row only: the rows that read it are spoilt in that dim alone
+    v[250, :, 4], k[250] = bad, 0
+    out = torch.empty_like(q)
+    kvq.kvq_prefill_attention(q, k, v, cu, out)
+    keep = [d for d in range(128) if d not in (3, 4)]
+    assert torch.isfinite(out[250:300][..., keep]).all() and not torch.isfinite(out[250:300, :, 3:5]).any()
+
+
+def test_rows_with_equal_scores(kvq, cuda):
+    """Zero queries: the mean of the values."""
+    def zero(q, k, v):
+        q.zero_()
+    _run(kvq, [400], 2, 2, "bf16", mutate=zero)
+
+
+def test_strided_rows_and_offsets_beyond_32_bits(kvq, cuda):
+    """q, k, v slices of one fused projection whose last rows lie beyond 2^31 elements."""
+    import torch
+    hq, hkv, lens = 8, 1, [150, 170]
+    n = 320
+    stride = 1 << 23  # 320 rows: 2.7e9 elements, 5.4 GB
+    buf = torch.empty(n * stride, dtype=torch.bfloat16, device="cuda")
+    qkv = buf.as_strided((n, hq + 2 * hkv, 128), (stride, 128, 1))
+    g = torch.Generator(device="cuda").manual_seed(8)
+    qkv.copy_(_rows(n, hq + 2 * hkv, "bf16", g))
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    out = torch.empty(n, 2 * hq, 128, dtype=torch.bfloat16, device="cuda")[:, 3:3 + hq]
+    kvq.kvq_prefill_attention(q, k, v, torch.tensor([0, 150, 320], dtype=torch.int32, device="cuda"), out)
+    want, tol = _reference(q, k, v, lens, [0, 150], [0, 0])
+    _close(out, want, tol)
+
+
+def test_bad_bounds_are_left_out(kvq, cuda):
+    """Descending bounds and bounds behind the rows: recorded, the other prompts computed, nothing else written."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, k, v = (_rows(200, 2, "bf16", g) for _ in range(3))
+    for cu, good in (([0, 60, 50, 120], [(0, 60), (50, 70)]), ([0, 90, 300], [(0, 90)]), ([-5, 20, 40], [(20, 20)])):
+        out = torch.full_like(q, 7.0)
+        kvq.kvq_prefill_attention(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), out)
+        assert kvq.kvq_last_device_status() == kvq.KVQ_ERR_OUT_OF_RANGE
+        left = torch.ones(200, dtype=torch.bool, device="cuda")
+        for s, n in good[::-1]:
+            left[s:s + n] = False
+        assert (out[left] == 7.0).all()
+        s, n = good[-1]
+        want, tol = _reference(q, k, v, [n], [s], [0])
+        _close(out[s + 10:s + n], want[s + 10:s + n], tol[s + 10:s + n])
+
+
+def test_empty_calls(kvq, cuda):
+    import torch
+    e = torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    kvq.kvq_prefill_attention(e, e, e, torch.zeros(3, dtype=torch.int32, device="cuda"), e)
+    x = torch.full((4, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = x.clone()
+    kvq.kvq_prefill_attention(x, x, x, torch.zeros(1, dtype=torch.int32, device="cuda"), out)
+    kvq.kvq_prefill_attention(x, x, x, torch.zeros(3, dtype=torch.int32, device="cuda"), out)
+    assert kvq.kvq_last_device_status() == 0 and (out == 7.0).all()
+
+
+def test_same_answer_again_and_in_graphs_on_two_streams(kvq, cuda):
+    """Calls repeat bit for bit, eager, captured and replayed next to each other."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q, k, v = _rows(700, 8, "bf16", g), _rows(700, 1, "bf16", g), _rows(700, 1, "bf16", g)
+    cu = torch.tensor([0, 100, 700], dtype=torch.int32, device="cuda")
+    opts = kvq.make_score_opts(softcap=30.0)
+    want = torch.empty_like(q)
+    kvq.kvq_prefill_attention(q, k, v, cu, want, opts=opts)
+    outs, graphs = [torch.empty_like(q) for _ in range(2)], []
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s, o in zip(streams, outs):
+        s.wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            kvq.kvq_prefill_attention(q, k, v, cu, o, opts=opts)
+    for _ in range(5):
+        for s, gr in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    cu.copy_(torch.tensor([0, 333, 650], dtype=torch.int32))  # other prompts through the same graph
+    kvq.kvq_prefill_attention(q, k, v, cu, want, opts=opts)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][:650], want[:650])
+    assert kvq.kvq_last_device_status() == 0
+
+
+def test_wrapper_refusals(kvq, cuda):
+    import torch
+    q, k = torch.zeros(6, 4, 128, device="cuda").half(), torch.zeros(6, 2, 128, device="cuda").half()
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    good = dict(q=q, k=k, v=k.clone(), cu_seqlens=cu, out=torch.empty_like(q))
+    kvq.kvq_prefill_attention(**good)
+    for bad in (dict(q=q.bfloat16()), dict(q=q[:5]), dict(k=k[:, :1]), dict(k=k.cpu()), dict(cu_seqlens=cu.long()),
+                dict(out=q), dict(out=torch.empty(6, 4, 128, device="cuda")), dict(q=q[:, :3]), dict(cu_seqlens=cu[:0]),
+                dict(v=k.transpose(1, 2).contiguous().transpose(1, 2)), dict(prefix_lens=torch.zeros_like(cu)),
+                dict(opts=kvq.make_score_opts(alibi_slopes=torch.ones(3, device="cuda"))),
+                dict(opts=kvq.make_score_opts(softcap=-1.0))):
+        with pytest.raises(kvq.KvqError):
+            kvq.kvq_prefill_attention(**{**good, **bad})

@@ -145,3 +145,26 @@ def test_scored_workspace_follows_the_window(kvq):
     assert w == kvq.kvq_decode_workspace_bytes(1024, 8, 2, 64, 1024 + 15) <= full
     assert kvq.kvq_decode_scored_workspace_bytes(1024, 8, 2, 64, 131072, window=2 ** 31 - 1) == full
     assert kvq.kvq_decode_scored_workspace_bytes(1024, 8, 2, 64, 131072, window=-1) == 0
+
+
+def test_prefill_refusals(kvq):
+    L = kvq.lib()
+
+    def call(o=None, **kw):
+        a = dict(q=P(0x10000), qs=512, k=P(0x20000), ks=256, v=P(0x30000), vs=256, out=P(0x40000), os=512, n=3, hq=4,
+                 hk=2, cu=P(0x5000), batch=1, prefix=None, dtype=kvq.KVQ_BF16)
+        a.update(kw)
+        return L.kvq_prefill_attention(ctypes.byref(o) if o is not None else None, *a.values(), None)
+
+    assert call(n=0) == kvq.KVQ_OK and call(batch=0) == kvq.KVQ_OK
+    for kw in (dict(n=-1), dict(batch=-1), dict(hq=0), dict(hk=0), dict(q=None), dict(k=P(0x20008)), dict(v=None),
+               dict(out=None), dict(cu=None), dict(qs=504), dict(ks=260), dict(vs=128), dict(os=0), dict(dtype=9),
+               dict(out=P(0x10000)), dict(out=P(0x20000)), dict(out=P(0x30000)), dict(ks=1 << 40)):
+        assert call(**kw) == kvq.KVQ_ERR_INVALID, kw
+    for kw in (dict(hq=6), dict(hq=5), dict(hq=32, qs=4096, os=4096), dict(dtype=kvq.KVQ_F32)):
+        assert call(**kw) == kvq.KVQ_ERR_UNSUPPORTED, kw
+    for bad in (dict(softcap=-1.0), dict(softcap=math.inf), dict(window=-1), dict(softmax_scale=math.nan)):
+        assert call(kvq.make_score_opts(**bad)) == kvq.KVQ_ERR_INVALID, bad
+    o = kvq.make_score_opts()
+    o.alibi_slopes = 0x1001
+    assert call(o) == kvq.KVQ_ERR_INVALID
