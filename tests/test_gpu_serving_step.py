@@ -1,0 +1,142 @@
+"""A serving loop from the library's parts, as an engine would run it: step
+tables, rotary positions, the write into the packed cache, prompt attention
+for the new prompts, then decode steps over the cache from one captured graph,
+with one sliding-window, softcapped model.  Against the definitions in 64 bits
+on the same cache; the plain bookkeeping is done again on the host."""
+import math
+
+import numpy as np
+import pytest
+
+import helpers
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+HQ, HKV, B, WIDTH, CAP, WINDOW, SOFTCAP = 16, 2, 16, 24, 96, 100, 30.0
+
+
+def _rotated(x, pos, turns, mag):
+    """Half layout, 64 bits, rounded to bf16 as the kernel's output is."""
+    import torch
+    phase = np.array([[(int(p) * int(t) % 2 ** 64) / 2 ** 64 for t in turns] for p in pos])
+    t = torch.from_numpy(2 * np.pi * phase)[:, None, :]
+    h = len(turns)
+    x = x.double().cpu()
+    a, b = x[..., :h], x[..., h:2 * h]
+    return torch.cat([mag * (a * t.cos() - b * t.sin()), mag * (b * t.cos() + a * t.sin()), x[..., 2 * h:]], -1)
+
+
+def _attend(q, k, v, t):
+    """One query [Hq, 128] at position t over keys 0 .. t (numpy, 64 bits)."""
+    lo = max(0, t - WINDOW + 1)
+    out = np.zeros((HQ, 128))
+    for h in range(HQ):
+        s = k[lo:t + 1, h * HKV // HQ] @ q[h] / math.sqrt(128)
+        s = SOFTCAP * np.tanh(s / SOFTCAP)
+        p = np.exp(s - s.max())
+        out[h] = p @ v[lo:t + 1, h * HKV // HQ] / p.sum()
+    return out
+
+
+def _cache_rows(pool, row, n):
+    """K and V of a sequence's n tokens from the pool's bytes, original domain."""
+    g = oracle.geom(num_blocks=CAP, num_kv_heads=HKV)
+    had = np.array([[1.0]])
+    while had.shape[0] < 128:
+        had = np.block([[had, had], [had, -had]])
+    had /= math.sqrt(128)
+    k, v = np.zeros((n, HKV, 128)), np.zeros((n, HKV, 128))
+    for t in range(n):
+        for h in range(HKV):
+            kc, sk, zk, vc, sv, zv = oracle.unpack_token(g, pool, int(row[t // B]), t % B, h)
+            k[t, h] = (kc * oracle.f16_to_f64(sk) + oracle.f16_to_f64(zk)) @ had
+            v[t, h] = (vc * oracle.f16_to_f64(sv) + oracle.f16_to_f64(zv)) @ had
+    return k, v
+
+
+def test_prompts_then_captured_decode_steps(kvq, cuda):
+    import torch
+    batch, rows = 3, 256
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool = kvq.new_pool(CAP, HKV)
+    ring = torch.randperm(CAP, generator=torch.Generator().manual_seed(1)).to(**i32)
+    state = torch.tensor([0, CAP, 0, 0], **i32)
+    lens, target = torch.zeros(batch, **i32), torch.tensor([120, 33, 1], **i32)
+    table, cu, maps = torch.full((batch, WIDTH), -1, **i32), torch.zeros(batch + 1, **i32), torch.zeros(3, rows, **i32)
+    desc = kvq.make_rope(64, 10000.0, False, "yarn", 4.0, 64, 1.0, 32.0)
+    turns, mag = kvq.kvq_rope_table(desc)
+    rope, _ = kvq.new_rope_table(desc)
+    opts = kvq.make_score_opts(softcap=SOFTCAP, window=WINDOW)
+    out = torch.zeros(rows, HQ, 128, dtype=torch.bfloat16, device="cuda")
+
+    # one fused projection's rows: q, k and v heads of each token
+    def project(n):
+        return torch.randn(n, HQ + 2 * HKV, 128, device="cuda", generator=gen).bfloat16()
+
+    def step(qkv, n):
+        """Tables, rotation (in place) and the write of a step of at most n tokens."""
+        kvq.kvq_update_tables(ring, state, state, lens, target, lens, table, cu, maps[0][:n], maps[1][:n], maps[2][:n])
+        kvq.kvq_rope(desc, rope, mag, maps[0][:n], qkv[:, :HQ], qkv[:, HQ:HQ + HKV])
+        kvq.kvq_quantize_append(pool, CAP, HKV, qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:], maps[2][:n],
+                                token_stride=(HQ + 2 * HKV) * 128)
+
+    qkv = project(rows)
+    raw = qkv.clone()
+    step(qkv, rows)
+    kvq.kvq_prefill_attention(qkv[:, :HQ], qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:], cu, out, opts=opts)
+    assert kvq.kvq_last_device_status() == 0
+    assert cu.tolist() == [0, 120, 153, 154] and lens.tolist() == [120, 33, 1]
+    pos = maps[0].cpu().numpy()
+    assert pos.tolist() == [*range(120), *range(33), 0] + [-1] * (rows - 154)
+    assert torch.equal(qkv[154:], raw[154:])
+    want = _rotated(raw[:154, :HQ + HKV], pos[:154], turns, mag)
+    got = qkv[:154, :HQ + HKV].double().cpu()
+    assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 6e-6).all()  # rounding; 6e-7 of |a| + |b| < 10
+    # the prompts' attention on the rotated rows: half a bf16 step (2^-8) of each p and of the output
+    x = qkv[:154].double().cpu().numpy()
+    k, v = x[:, HQ:HQ + HKV], x[:, HQ + HKV:]
+    o = out.double().cpu().numpy()
+    for s, n in ((0, 120), (120, 33), (153, 1)):
+        for t in range(n):
+            w = _attend(x[s + t, :HQ], k[s:s + n], v[s:s + n], t)
+            assert np.abs(o[s + t] - w).max() <= 2 * 2.0 ** -8 * np.abs(v[s:s + t + 1]).max() + 1e-4
+
+    # decode: one graph, three requests of which the second ends and starts again from nothing
+    qkv1, out1 = project(batch), torch.zeros(batch, HQ, 128, dtype=torch.bfloat16, device="cuda")
+    ws = kvq.new_scored_workspace(CAP, HKV, batch, HQ, WIDTH * B, window=WINDOW)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(qkv1, batch)
+        kvq.kvq_decode_attention_scored(pool, CAP, HKV, qkv1[:, :HQ].contiguous(), table, lens, WIDTH * B, out1, ws,
+                                        opts)
+    for i in range(20):
+        target.copy_(lens + 1)
+        if i == 7:
+            target[1] = 0  # finished: its blocks go back, its output is zero
+        qkv1.copy_(project(batch))
+        graph.replay()
+        assert kvq.kvq_last_device_status() == 0
+        now = lens.tolist()
+        assert now == [121 + i, 0 if i == 7 else (34 + i if i < 7 else i - 7), 2 + i]
+        if i in (0, 6, 7, 8, 19):
+            bytes_, rows_ = pool.cpu().numpy(), table.cpu().numpy()
+            order = [b for b in range(batch) if now[b] > 0]  # packed rows of the step, by sequence
+            q = qkv1.double().cpu().numpy()
+            for b in range(batch):
+                if now[b] == 0:
+                    assert not out1[b].any()
+            if len(order) == batch:
+                for b in order:
+                    ck, cv = _cache_rows(bytes_, rows_[b], now[b])
+                    w = _attend(q[b, :HQ], ck, cv, now[b] - 1)
+                    err = np.abs(out1[b].double().cpu().numpy() - w) - 2.0 ** -8 * np.abs(w)
+                    assert err.max() <= helpers.ATTN_TOL
+        # no block is owned twice, none is lost
+        s = state.tolist()
+        free = [ring[(s[0] + j) % CAP].item() for j in range(s[1])]
+        owned = [p for b in range(batch) for p in table[b, :-(-now[b] // B)].tolist()]
+        assert sorted(free + owned) == list(range(CAP))
