@@ -579,13 +579,23 @@ int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_s
   const float tau = opts->softmax_scale > 0.0f ? opts->softmax_scale : 0.08838834764831844055f;
   a.scale_log2 = tau * 1.4426950408889634074f;
   a.softcap = opts->softcap * 1.4426950408889634074f;
-  a.softcap_exp = opts->softcap > 0.0f ? 2.0f * a.scale_log2 / opts->softcap : 0.0f;
+  a.cap_inv = opts->softcap > 0.0f ? std::min(tau / opts->softcap, 1e30f) : 0.0f;
+  // (for a cap so small that a coefficient would pass fp32, only a zero counts as near)
+  a.cap_test = a.cap_inv <= 1000.0f ? a.cap_inv : 3e38f;
+  static const double half[4] = {0.99999945103, -0.33326284231, 0.13189939426, -0.044392738432};
+  static const double one[7] = {0.99999994865, -0.33332827979, 0.13325076146, -0.05345164637,
+                                0.020279708285, -0.0061943248336, 0.0010380250967};
+  double power = a.scale_log2;
+  for (int x = 0; x < 7; ++x, power *= static_cast<double>(a.cap_inv) * a.cap_inv) {
+    a.cap_one[x] = static_cast<float>(std::min(std::max(power * one[x], -1e38), 1e38));
+    if (x < 4) a.cap_half[x] = static_cast<float>(std::min(std::max(power * half[x], -1e38), 1e38));
+  }
   a.window = opts->window;
   a.alibi_slopes = opts->alibi_slopes;
   a.status = device_status_ptr();
   if (!a.status) return KVQ_ERR_CUDA;
-  const int64_t ctas = ((static_cast<int64_t>(n_tokens) * group / 256) + batch) * num_kv_heads;
-  if (ctas > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  const int64_t items = ((static_cast<int64_t>(n_tokens) * group / 256) + batch) * num_kv_heads;
+  if (items > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
   return launch_prefill(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 

@@ -356,8 +356,9 @@ struct PrefillArgs {
   int32_t batch;
   const int32_t* prefix_lens;  // or nullptr
   float scale_log2;            // softmax scale times log2(e)
-  // score options as in DecodeArgs, but softcap_exp takes the raw product q.k
-  float softcap, softcap_exp;
+  float softcap;               // cap log2(e); 0: no cap
+  float cap_inv, cap_test;     // softmax scale / cap; what chooses between the capped score's forms
+  float cap_half[4], cap_one[7];  // coefficients of the capped score for |s / cap| up to 1/2, 1
   int32_t window;
   const float* alibi_slopes;
   int* status;

@@ -39,36 +39,57 @@
 #include <cuda.h>
 #include <math_constants.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "kvq_internal.cuh"
 
+#ifndef POLY
+#define POLY 2
+#endif
+#ifndef POLYB
+#define POLYB 0
+#endif
 namespace kvq {
 namespace {
 
 constexpr int kTile = 128;         // rows of a product, keys of a tile
-constexpr int kStages = 5;         // K and V tiles in shared memory
+constexpr int kHalf = kTile / 2;
+constexpr int kStages = 4;         // K and V tiles in shared memory
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kHalfBytes = kTileBytes / 2;  // 64 of the 128 dims: one swizzle width
-constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSoftWarps = 8;      // four a tile
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;
 constexpr int kThreads = 384;
+constexpr int kItems = 2;          // items handed out ahead
+constexpr int kItemReaders = kSoftWarps + 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per tile
 constexpr float kLazy = 8.0f;      // log2 of the largest p
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // a device-side wait gives up after one second
 
+// The rows of a prompt's 256 / G tokens and one kv head: what a CTA works on.
+struct Item {
+  int row0, n;     // the prompt's first row and length; n < 0: no more items
+  int prefix;      // keys that every query reads
+  int t0;          // first token
+  int kv_head;
+};
+
 struct __align__(1024) Smem {
   uint8_t q[2][kTileBytes];
   uint8_t kv[kStages][kTileBytes];
-  uint64_t q_full[2];
+  uint8_t out[kSoftWarps][32 * kHeadDim];  // per warp: 32 rows of half the output, on their way to memory
+  uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t s_full[2];  // S of the tile is written (and every product before it is complete)
-  uint64_t p_full[2];  // P of the tile is written, O rescaled
+  uint64_t p_half[2], p_full[2];  // P of the tile's first 64 keys, of all, is written (O rescaled)
   uint64_t o_full[2];  // O of the tile is final
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t fin;        // every product issued is complete
+  Item item[kItems];
   uint32_t tmem_base;
   int abort;           // a wait ran out: every other wait gives up at once
-  int seq, tile;       // this CTA's item
-  int red[2][kThreads / 32];
 };
 constexpr int kSmemBytes = static_cast<int>(sizeof(Smem));
 static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
@@ -102,7 +123,7 @@ __device__ __forceinline__ uint64_t global_ns() {
 // Bounded, warp-uniform wait for a barrier phase: false if it did not come
 // within the limit or another warp already gave up.  `abort` may be null (a
 // last wait, which ignores the others' failure).
-__device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint64_t t0 = global_ns();
   for (uint32_t it = 1;; ++it) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -120,10 +141,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
 
 // A box of a tensor map into this CTA's shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -158,18 +175,34 @@ constexpr uint32_t idesc(bool vmajor) {
   return (1u << 4) | ((kBF16 ? 1u : 0u) << 7) | ((kBF16 ? 1u : 0u) << 10) | ((vmajor ? 1u : 0u) << 16) |
          ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+// One thread issues the products, but its warp walks them together: the
+// instructions are predicated, not branched around, so that descriptors and
+// addresses stay in uniform registers (behind `if (lane == 0)` each product
+// took about 120 clocks to issue, more than the 64 that it runs).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %3, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(static_cast<uint32_t>(acc)), "r"(id)
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(acc)), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %3, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(static_cast<uint32_t>(acc)), "r"(id)
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(acc)), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar)),
+      "r"(elected)
       : "memory");
 }
 
@@ -187,18 +220,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -215,6 +246,60 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x (MUFU.EX2); ex2(-inf) = 
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+typedef unsigned long long u64x;
+__device__ __forceinline__ u64x pk2(float a, float b) {
+  u64x r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk2(u64x v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ u64x add2(u64x a, u64x b) {
+  u64x d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64x mul2(u64x a, u64x b) {
+  u64x d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64x fma2(u64x a, u64x b, u64x c) {
+  u64x d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// 2^x of two x <= kLazy on the FMA pipe: x = n + f with n the nearest integer,
+// 2^f by interpolation at the Chebyshev points of [-1/2, 1/2], n added to the
+// exponent.  Degree 3 is off by 1.0e-4, 1/20 of the half step of bf16, degree
+// 4 by 3.5e-6, 1/70 of that of fp16.  An x below -126 gives 2^-126, so masked
+// places do not come here.
+template <bool kBF16>
+__device__ __forceinline__ void ex2_fma(u64x x, float& p0, float& p1) {
+  auto c = [](float v) { return pk2(v, v); };
+  float x0, x1;
+  upk2(x, x0, x1);
+  x = pk2(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
+  const u64x t = add2(x, c(12582912.0f));  // 1.5 * 2^23: the low bits hold n
+  const u64x f = fma2(add2(t, c(-12582912.0f)), c(-1.0f), x);
+  u64x p;
+  if (kBF16) {
+    p = fma2(c(0.0558382829f), f, c(0.2426394785f));
+    p = fma2(p, f, c(0.6931367338f));
+    p = fma2(p, f, c(0.9999245570f));
+  } else {
+    p = fma2(c(0.0096663685f), f, c(0.0559219758f));
+    p = fma2(p, f, c(0.2402234904f));
+    p = fma2(p, f, c(0.6931210452f));
+    p = fma2(p, f, c(1.0f));
+  }
+  float a, b, n0, n1;
+  upk2(p, a, b);
+  upk2(t, n0, n1);
+  p0 = __int_as_float(__float_as_int(a) + (__float_as_int(n0) << 23));
+  p1 = __int_as_float(__float_as_int(b) + (__float_as_int(n1) << 23));
 }
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
@@ -236,123 +321,208 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// cap tanh(s / cap) in base-2 units (cap_exp = 2 / (cap ln 2), cap2 = cap log2 e):
-// tanh(x) = 1 - 2 / (e^2x + 1), an absolute error of about 2^-22 cap.
-__device__ __forceinline__ float capped(float s, float cap_exp, float cap2) {
+// Softcap: y = cap tanh(s / cap) in base-2 units from the raw product d, by the
+// largest |x|, x = d cap_inv = s / cap, of the warp's rows:
+//   |x| <= 1/2 or 1: y = d T(d^2), T of degree 3 or 6 the interpolation of
+//     tanh(sqrt u) / sqrt u at the Chebyshev points of [0, 1/4] or [0, 1], off
+//     by 5.5e-7 or 5.2e-8 of itself, so right for caps of any size; five or
+//     eight packed operations a pair of scores, the cap and the softmax scale
+//     in the coefficients;
+//   beyond: y = cap (1 - 2 / (e^2x + 1)), off by 2^-22 cap; four of the MUFU's
+//     a pair, 32 clocks a warp where the FMA pipe takes 10 or 16.
+__device__ __forceinline__ float capped_far(float d, const PrefillArgs& a) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * cap_exp) + 1.0f));
-  return fmaf(-2.0f * cap2, r, cap2);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(d * (a.cap_inv * 2.8853900817779268f)) + 1.0f));  // 2^(2x log2 e)
+  return fmaf(-2.0f * a.softcap, r, a.softcap);
+}
+template <int kN>
+__device__ __forceinline__ void capped_near(float (&s)[kTile], const float (&coef)[kN]) {
+#pragma unroll
+  for (int e = 0; e < kTile; e += 2) {
+    const u64x d = pk2(s[e], s[e + 1]), u = mul2(d, d);
+    u64x p = pk2(coef[kN - 1], coef[kN - 1]);
+#pragma unroll
+    for (int x = kN - 2; x >= 0; --x) p = fma2(p, u, pk2(coef[x], coef[x]));
+    upk2(mul2(d, p), s[e], s[e + 1]);
+  }
+}
+__device__ __forceinline__ void cap_scores(float (&s)[kTile], const PrefillArgs& a) {
+  float big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < kTile; e += 2) big[(e >> 1) & 3] = max3f(big[(e >> 1) & 3], fabsf(s[e]), fabsf(s[e + 1]));
+  const float x = fmaxf(max3f(big[0], big[1], big[2]), big[3]) * a.cap_test;
+  if (!__any_sync(0xffffffffu, x > 0.5f)) {
+    capped_near(s, a.cap_half);
+  } else if (!__any_sync(0xffffffffu, x > 1.0f)) {
+    capped_near(s, a.cap_one);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kTile; ++e) s[e] = capped_far(s[e], a);
+  }
+}
+__device__ __forceinline__ float capped(float d, const PrefillArgs& a) {
+  if (fabsf(d) * a.cap_test > 1.0f) return capped_far(d, a);
+  const float u = d * d;
+  float p = a.cap_one[6];
+#pragma unroll
+  for (int x = 5; x >= 0; --x) p = fmaf(p, u, a.cap_one[x]);
+  return d * p;
 }
 
-// The key interval [lo, hi) of the query at position t of a prompt of n tokens.
+// The key interval [lo, hi) of the query at position t of a prompt.
 struct Span {
-  int n, prefix, window;
+  int prefix, window;
   __device__ __forceinline__ int lo(int t) const { return window > 0 ? max(t - window + 1, 0) : 0; }
   __device__ __forceinline__ int hi(int t) const { return max(t + 1, prefix); }
 };
 
-// A row whose output is not finite though its l is: one warp looks for a value
-// that is not finite among the masked keys [k0, k1) - [lo, hi) that the row's
-// products read, and if there is one forms the output again over [lo, hi).
-// True if it wrote the row.
+// An item's two row tiles and the key tiles that each reads, [klo, khi), walked
+// from the newest to the oldest in `steps` steps; the second tile may have no token.
+struct Walk {
+  Span sp;
+  int first[2], last[2];  // tokens of each tile
+  int klo[2], khi[2];
+  int top, steps;
+  bool two;
+  __device__ __forceinline__ Walk(const Item& it, int window, int tile_tokens) {
+    sp.prefix = it.prefix;
+    sp.window = window;
+    two = it.t0 + tile_tokens < it.n;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      first[i] = it.t0 + i * tile_tokens;
+      last[i] = min(first[i] + tile_tokens, it.n) - 1;
+      klo[i] = sp.lo(first[i]) / kTile;
+      khi[i] = (sp.hi(last[i]) + kTile - 1) / kTile;
+    }
+    if (!two) khi[1] = klo[1] = klo[0];
+    top = max(khi[0], khi[1]);
+    steps = top - klo[0];
+  }
+  __device__ __forceinline__ bool active(int i, int c) const { return top - 1 - c >= klo[i] && top - 1 - c < khi[i]; }
+};
+
+// 64 dims (half hf) of a row whose output is not finite there though its l is:
+// one warp looks for a value that is not finite among the masked keys [k0, k1)
+// - [lo, hi) that the row's products read, and if there is one forms the output
+// again over [lo, hi).
 template <bool kBF16>
-__device__ __noinline__ bool fix_row(const PrefillArgs& a, int64_t row0, int t, int head, int kv_head, int k0, int k1,
-                                     int lo, int hi, float slope2, float m, float l) {
+__device__ __forceinline__ void fix_row(const PrefillArgs& a, int64_t row0, int t, int head, int kv_head, int hf, int k0,
+                                        int k1, int lo, int hi, float slope2, float m, float l) {
   const int lane = threadIdx.x & 31;
   auto four = [&](const uint16_t* base, int64_t stride, int64_t r, int h) {
     const uint2 w = *reinterpret_cast<const uint2*>(base + r * stride + h * kHeadDim + 4 * lane);
     const float2 x = unpack2<kBF16>(w.x), y = unpack2<kBF16>(w.y);
     return make_float4(x.x, x.y, y.x, y.y);
   };
+  auto value = [&](int j) {
+    return unpack2<kBF16>(*reinterpret_cast<const uint32_t*>(a.v + (row0 + j) * a.v_stride + kv_head * kHeadDim +
+                                                             kHalf * hf + 2 * lane));
+  };
   bool found = false;
   for (int j = k0; j < k1 && !found; ++j) {
     if (j == lo) j = hi;
     if (j >= k1) break;
-    const float4 v = four(a.v, a.v_stride, row0 + j, kv_head);
-    found = __any_sync(0xffffffffu, !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w)));
+    const float2 v = value(j);
+    found = __any_sync(0xffffffffu, !(isfinite(v.x) && isfinite(v.y)));
   }
-  if (!found) return false;
+  if (!found) return;
   const float4 q = four(a.q, a.q_stride, row0 + t, head);
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float2 o = make_float2(0.0f, 0.0f);
   for (int j = lo; j < hi; ++j) {
     const float4 k = four(a.k, a.k_stride, row0 + j, kv_head);
     float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
 #pragma unroll
     for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    float y = a.softcap > 0.0f ? capped(s, a.softcap_exp, a.softcap) : s * a.scale_log2;
+    float y = a.softcap > 0.0f ? capped(s, a) : s * a.scale_log2;
     y = fmaf(-slope2, fabsf(static_cast<float>(t - j)), y);
     const float p = ex2(y - m);
-    const float4 v = four(a.v, a.v_stride, row0 + j, kv_head);
+    const float2 v = value(j);
     o.x = fmaf(p, v.x, o.x);
     o.y = fmaf(p, v.y, o.y);
-    o.z = fmaf(p, v.z, o.z);
-    o.w = fmaf(p, v.w, o.w);
   }
   const float inv = 1.0f / l;
-  *reinterpret_cast<uint2*>(a.out + (row0 + t) * a.out_stride + head * kHeadDim + 4 * lane) =
-      make_uint2(pack2<kBF16>(o.x * inv, o.y * inv), pack2<kBF16>(o.z * inv, o.w * inv));
-  return true;
+  *reinterpret_cast<uint32_t*>(a.out + (row0 + t) * a.out_stride + head * kHeadDim + kHalf * hf + 2 * lane) =
+      pack2<kBF16>(o.x * inv, o.y * inv);
 }
 
-// This CTA's item by its rank among the items in falling order of tile index
-// (ties by prompt): sm.seq and sm.tile, or seq = -1.  Every thread calls.
-// Prompt b has ceil(length / tokens) tiles; one whose bounds are not ascending
-// or not within the rows has none and is recorded.
-__device__ __forceinline__ void find_item(const PrefillArgs& a, Smem& sm, int rank, int tokens, int log_tokens) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-  auto tiles = [&](int b) {
+// The items of a CTA, found by one warp ahead of the others.  Prompt b has
+// ceil(length / 256 * G) row tile pairs (one whose bounds are not ascending or
+// not within the rows has none and is recorded); the items, in falling order of
+// the pair's index, ties by prompt, then by kv head, are dealt out to the CTAs
+// back and forth, so that each gets about the same sum.
+struct Items {
+  const PrefillArgs& a;
+  const int lane, log_tokens;
+  int mine;   // pairs of prompt `lane` (all that is needed up to 32 prompts)
+  int bound;  // no prompt has more pairs
+  __device__ __forceinline__ int tiles(int b) const {
     const int s = __ldg(a.cu_seqlens + b), e = __ldg(a.cu_seqlens + b + 1);
-    return s >= 0 && e >= s && e <= a.n_tokens ? (e - s + tokens - 1) >> log_tokens : -1;
-  };
-  int step = 0;
-  // items with a tile index >= i
-  auto count = [&](int i) {
-    int c = 0;
-    for (int b = b0; b < b1; ++b) c += max(tiles(b) - i, 0);
-    c = __reduce_add_sync(0xffffffffu, c);
-    int* red = sm.red[step++ & 1];
-    if (lane == 0) red[warp] = c;
-    __syncthreads();
-    c = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) c += red[w];
-    return c;
-  };
-  if (blockIdx.x == 0)
-    for (int b = b0; b < b1; ++b)
-      if (tiles(b) < 0) record_status(a.status, KVQ_ERR_OUT_OF_RANGE);
-  if (tid == 0) sm.seq = -1;
-  if (rank >= count(0)) return;
-  int lo = 0, hi = (a.n_tokens >> log_tokens) + 2;  // count(lo) > rank >= count(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (count(mid) > rank)
-      lo = mid;
-    else
-      hi = mid;
+    return s >= 0 && e >= s && e <= a.n_tokens ? (e - s + (1 << log_tokens) - 1) >> log_tokens : -1;
   }
-  const int k = rank - count(lo + 1);  // my place among the prompts with more than lo tiles
-  int c = 0;
-  for (int b = b0; b < b1; ++b) c += tiles(b) > lo ? 1 : 0;
-  int inc = c;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += up;
+  // pairs with an index >= i
+  __device__ __forceinline__ int count(int i) const {
+    int c = max(mine - i, 0);
+    for (int b = 32 + lane; b < a.batch; b += 32) c += max(tiles(b) - i, 0);
+    return __reduce_add_sync(0xffffffffu, c);
   }
-  int* red = sm.red[step & 1];
-  if (lane == 31) red[warp] = inc;
-  __syncthreads();
-  int at = inc - c;
-  for (int w = 0; w < warp; ++w) at += red[w];
-  for (int b = b0; b < b1; ++b)
-    if (tiles(b) > lo && at++ == k) {
-      sm.seq = b;
-      sm.tile = lo;
+  __device__ __forceinline__ Items(const PrefillArgs& args, int log_t)
+      : a(args), lane(threadIdx.x & 31), log_tokens(log_t), mine(0) {
+    bool bad = false;
+    int most = 0;
+    for (int b = lane; b < a.batch; b += 32) {
+      const int n = tiles(b);
+      if (b < 32) mine = n;
+      bad |= n < 0;
+      most = max(most, n);
     }
-}
+    bound = __reduce_max_sync(0xffffffffu, most);
+    if (bad && blockIdx.x == 0) record_status(a.status, KVQ_ERR_OUT_OF_RANGE);
+  }
+  // the item of rank `rank` among the pairs; false if there is none.  Ranks rise
+  // from call to call, so the index searched for only falls.
+  __device__ __forceinline__ bool find(int rank, Item* it) {
+    int lo = 0, hi = bound;  // count(lo) > rank >= count(hi)
+    if (rank >= count(0)) return false;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (count(mid) > rank)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    bound = lo + 1;
+    int k = rank - count(lo + 1);  // my place among the prompts with more than lo pairs
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const uint32_t has = __ballot_sync(0xffffffffu, b < a.batch && (b0 == 0 ? mine : tiles(b)) > lo);
+      if (k >= __popc(has)) {
+        k -= __popc(has);
+        continue;
+      }
+      const bool me = ((has >> lane) & 1u) != 0 && __popc(has & ((1u << lane) - 1u)) == k;
+      const int at = b0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+      it->row0 = __ldg(a.cu_seqlens + at);
+      it->n = __ldg(a.cu_seqlens + at + 1) - it->row0;
+      it->prefix = a.prefix_lens != nullptr ? min(__ldg(a.prefix_lens + at), it->n) : 0;
+      it->t0 = lo << log_tokens;
+      return true;
+    }
+    return false;
+  }
+};
+
+// A ring position and the parity of its present use.
+template <int kN>
+struct Ring {
+  uint32_t i = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == kN) {
+      i = 0;
+      ph ^= 1u;
+    }
+  }
+};
 
 template <bool kBF16, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
@@ -366,6 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == kLoadWarp) {
+    if (lane < 3)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.map_q : lane == 1 ? &a.map_k : &a.map_v) : "memory");
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < kStages; ++i) {
@@ -375,9 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.q_full[i], 1);
+        mbar_init(&sm.q_empty[i], 1);
         mbar_init(&sm.s_full[i], 1);
+        mbar_init(&sm.p_half[i], kSoftWarps / 2);
         mbar_init(&sm.p_full[i], kSoftWarps / 2);
         mbar_init(&sm.o_full[i], 1);
+      }
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        mbar_init(&sm.item_full[i], 1);
+        mbar_init(&sm.item_empty[i], kItemReaders);
       }
       mbar_init(&sm.fin, 1);
       sm.abort = 0;
@@ -385,181 +564,210 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     __syncwarp();
   }
-  pdl_wait();
-  const int log_g = a.log_group, log_tokens = 8 - log_g, tile_tokens = kTile >> log_g;
-  const int kv_head = blockIdx.x % a.num_kv_heads;
-  find_item(a, sm, blockIdx.x / a.num_kv_heads, 2 * tile_tokens, log_tokens);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   const uint32_t tbase = sm.tmem_base;
-  const int seq = sm.seq;
+  const int log_g = a.log_group, log_tokens = 8 - log_g, tile_tokens = kTile >> log_g;
   bool bad = false;
-  if (seq >= 0) {
-    const int t0 = sm.tile << log_tokens;
-    const int64_t row0 = __ldg(a.cu_seqlens + seq);
-    Span sp;
-    sp.n = __ldg(a.cu_seqlens + seq + 1) - static_cast<int>(row0);
-    sp.window = a.window;
-    sp.prefix = a.prefix_lens != nullptr ? min(__ldg(a.prefix_lens + seq), sp.n) : 0;
-    // key tiles [klo, khi) of each row tile; the second may have no token
-    const bool two = t0 + tile_tokens < sp.n;
-    int klo[2], khi[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int first = t0 + i * tile_tokens, last = min(first + tile_tokens, sp.n) - 1;
-      klo[i] = sp.lo(first) / kTile;
-      khi[i] = (sp.hi(last) + kTile - 1) / kTile;
-      if (i == 1 && !two) khi[i] = klo[i] = klo[0];
+  // the next item of a reader's ring; false behind the last one or after a wait that gave up
+  auto next_item = [&](Ring<kItems>& r, Item* it) {
+    if (!mbar_wait(&sm.item_full[r.i], r.ph, abort)) {
+      bad = true;
+      return false;
     }
-    const int top = max(khi[0], khi[1]), steps = top - klo[0];
-    auto active = [&](int i, int c) { return top - 1 - c >= klo[i] && top - 1 - c < khi[i]; };
+    *it = sm.item[r.i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[r.i]);
+    r.next();
+    return it->n >= 0;
+  };
 
-    if (warp == kLoadWarp) {
-      auto box_q = [&](int i) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.q_full[i], kTileBytes);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            tma_load4(smem_u32(sm.q[i]) + hf * kHalfBytes, &a.map_q, 64 * hf, 0, kv_head,
-                      static_cast<int>(row0) + t0 + i * tile_tokens, &sm.q_full[i]);
-        }
-        __syncwarp();
-      };
-      int st = 0;
-      uint32_t ph = 0;
-      bool live = true;
-      box_q(0);
-      for (int x = 0; x < 2 * steps && live; ++x) {  // K and V of step x / 2
-        if (x >= kStages && !mbar_wait(&sm.kv_empty[st], ph ^ 1u, abort)) {
+  // registers: 3 x 168 a thread at launch, 72 + 2 x 216 from here
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kItemWarp) {
+      Items items(a, log_tokens);
+      Ring<kItems> r;
+      const uint32_t ctas = gridDim.x;
+      for (uint32_t k = 0;; ++k) {
+        const uint32_t n = k * ctas + (k & 1u ? ctas - 1u - blockIdx.x : blockIdx.x);
+        Item it;
+        it.kv_head = static_cast<int>(n % a.num_kv_heads);
+        const bool live = items.find(static_cast<int>(n / a.num_kv_heads), &it);
+        if (!live) it.n = -1;
+        if (k >= kItems && !mbar_wait(&sm.item_empty[r.i], r.ph ^ 1u, abort)) {
           bad = true;
-          live = false;  // no copy is issued any more
           break;
         }
         if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.kv_full[st], kTileBytes);
-          const CUtensorMap* map = x & 1 ? &a.map_v : &a.map_k;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            tma_load3(smem_u32(sm.kv[st]) + hf * kHalfBytes, map, 64 * hf, kv_head,
-                      static_cast<int>(row0) + (top - 1 - x / 2) * kTile, &sm.kv_full[st]);
+          sm.item[r.i] = it;
+          mbar_arrive(&sm.item_full[r.i]);
         }
         __syncwarp();
-        if (x == 0 && two) box_q(1);
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1u;
-        }
-        // after the last copy, or a wait that gave up: the copies still in
-        // flight land before the CTA gives up its shared memory (below)
+        if (!live) break;
+        r.next();
       }
-      // the last copy into each stage, newest first
-      for (int x = 0; x < kStages && x < 2 * steps; ++x) {
-        if (--st < 0) {
-          st = kStages - 1;
-          ph ^= 1u;
-        }
-        if (!mbar_wait_slow(&sm.kv_full[st], ph, nullptr)) bad = true;
-      }
-      if (!mbar_wait_slow(&sm.q_full[0], 0, nullptr)) bad = true;
-      if (two && !mbar_wait_slow(&sm.q_full[1], 0, nullptr)) bad = true;
-    } else if (warp == kMmaWarp) {
-      const uint32_t q0 = smem_u32(sm.q[0]), kv0 = smem_u32(sm.kv[0]);
-      int st = 0;
-      uint32_t ph = 0;
-      uint32_t pph[2] = {0, 0};
-      bool started[2] = {false, false};
-      auto next = [&] {
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1u;
-        }
-      };
-      auto product_s = [&](int i, int stage) {
-        if (lane == 0) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint32_t off = (s >> 2) * kHalfBytes + (s & 3) * 32;
-            mma_ss(tbase + kColS + 128 * i, sdesc(q0 + i * kTileBytes + off, 16), sdesc(kv0 + stage * kTileBytes + off, 16),
-                   idesc<kBF16>(false), s > 0);
+    } else if (warp == kLoadWarp) {
+      Ring<kItems> ri;
+      Ring<kStages> rk;
+      uint32_t copies = 0, nq[2] = {0, 0};
+      Item it;
+      while (!bad && next_item(ri, &it)) {
+        const Walk w(it, a.window, tile_tokens);
+        auto box_q = [&](int i) {
+          if (nq[i] > 0 && !mbar_wait(&sm.q_empty[i], (nq[i] - 1) & 1u, abort)) {
+            bad = true;
+            return;
           }
-          mma_commit(&sm.s_full[i]);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.q_full[i], kTileBytes);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              tma_load4(smem_u32(sm.q[i]) + hf * kHalfBytes, &a.map_q, 64 * hf, 0, it.kv_head, it.row0 + w.first[i],
+                        &sm.q_full[i]);
+          }
+          __syncwarp();
+          ++nq[i];
+        };
+        box_q(0);
+        for (int x = 0; x < 2 * w.steps && !bad; ++x) {  // K and V of step x / 2
+          if (copies >= kStages && !mbar_wait(&sm.kv_empty[rk.i], rk.ph ^ 1u, abort)) {
+            bad = true;  // no copy is issued any more
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.kv_full[rk.i], kTileBytes);
+            const CUtensorMap* map = x & 1 ? &a.map_v : &a.map_k;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              tma_load3(smem_u32(sm.kv[rk.i]) + hf * kHalfBytes, map, 64 * hf, it.kv_head,
+                        it.row0 + (w.top - 1 - x / 2) * kTile, &sm.kv_full[rk.i]);
+          }
+          __syncwarp();
+          ++copies;
+          rk.next();
+          if (x == 0 && w.two) box_q(1);
         }
-        __syncwarp();
-      };
+      }
+      // The copies still in flight (after a wait that gave up; else none) land
+      // before the CTA gives up its shared memory: the last one into each
+      // stage, newest first, and into each query tile.
+      for (uint32_t x = 0; x < kStages && x < copies; ++x) {
+        if (rk.i == 0) {
+          rk.i = kStages;
+          rk.ph ^= 1u;
+        }
+        --rk.i;
+        if (!mbar_wait_slow(&sm.kv_full[rk.i], rk.ph, nullptr)) bad = true;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (nq[i] > 0 && !mbar_wait_slow(&sm.q_full[i], (nq[i] - 1) & 1u, nullptr)) bad = true;
+    } else if (warp == kMmaWarp) {
+      // descriptors move by 16 bytes a unit: 16 dims (Q, K) 2, 64 dims 1024,
+      // 16 tokens of V 128, a tile 2048
+      const uint64_t dq = sdesc(smem_u32(sm.q[0]), 16), dk = sdesc(smem_u32(sm.kv[0]), 16);
+      const uint64_t dv = sdesc(smem_u32(sm.kv[0]), kHalfBytes);
+      const uint32_t elected = elect_one();
+      Ring<kItems> ri;
+      Ring<kStages> rk;
+      uint32_t pph = 0, qph = 0;  // bit i: parity of tile i's next P, next Q
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!mbar_wait(bar, parity, abort)) bad = true;
       };
-      wait(&sm.q_full[0], 0);
-      if (two) wait(&sm.q_full[1], 0);
-      wait(&sm.kv_full[0], 0);
-      tc_fence_after();
+      Item it;
+      while (!bad && next_item(ri, &it)) {
+        const Walk w(it, a.window, tile_tokens);
+        bool started[2] = {false, false};
+        // S of tile i with the keys in `stage`, walked at step c
+        auto product_s = [&](int i, uint32_t stage, int c) {
+          const uint64_t x = dq + 2048u * i, y = dk + 2048u * stage;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (active(i, 0)) product_s(i, 0);
-      if (lane == 0) mma_commit(&sm.kv_empty[0]);
-      __syncwarp();
-      next();
-#pragma unroll 1
-      for (int c = 0; c < steps; ++c) {
-        const int sv = st;
-        wait(&sm.kv_full[st], ph);
-        next();
-        const bool more = c + 1 < steps;
-        const int sk = st;
-        bool have_k = false;
+          for (int s = 0; s < 8; ++s) {
+            const uint32_t off = (s >> 2) * 1024 + (s & 3) * 2;
+            mma_ss(elected, tbase + kColS + 128 * i, x + off, y + off, idesc<kBF16>(false), s > 0);
+          }
+          mma_commit(elected, &sm.s_full[i]);
+          if (c + 1 >= w.steps || !w.active(i, c + 1)) mma_commit(elected, &sm.q_empty[i]);
+        };
+        wait(&sm.kv_full[rk.i], rk.ph);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (active(i, c)) {
-            wait(&sm.p_full[i], pph[i]);
-            pph[i] ^= 1u;
-            tc_fence_after();
-            if (lane == 0) {
+          if (i == 0 || w.two) {
+            wait(&sm.q_full[i], (qph >> i) & 1u);
+            qph ^= 1u << i;
+          }
+          tc_fence_after();
+          if (w.active(i, 0)) product_s(i, rk.i, 0);
+        }
+        mma_commit(elected, &sm.kv_empty[rk.i]);
+        rk.next();
+#pragma unroll 1
+        for (int c = 0; c < w.steps; ++c) {
+          const uint32_t sv = rk.i;
+          wait(&sm.kv_full[sv], rk.ph);
+          rk.next();
+          const bool more = c + 1 < w.steps;
+          const uint32_t sk = rk.i;
+          if (more) wait(&sm.kv_full[sk], rk.ph);
 #pragma unroll
-              for (int s = 0; s < 8; ++s)
-                mma_ts(tbase + kColO + 128 * i, tbase + kColS + 128 * i + 8 * s,
-                       sdesc(kv0 + sv * kTileBytes + 2048 * s, kHalfBytes), idesc<kBF16>(true), started[i] || s > 0);
-              if (!more || !active(i, c + 1)) mma_commit(&sm.o_full[i]);
+          for (int i = 0; i < 2; ++i) {
+            if (w.active(i, c)) {
+              const uint64_t y = dv + 2048u * sv;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                wait(hf == 0 ? &sm.p_half[i] : &sm.p_full[i], (pph >> i) & 1u);
+                tc_fence_after();
+#pragma unroll
+                for (int s = 4 * hf; s < 4 * hf + 4; ++s)
+                  mma_ts(elected, tbase + kColO + 128 * i, tbase + kColS + 128 * i + 8 * s, y + 128 * s,
+                         idesc<kBF16>(true), started[i] || s > 0);
+              }
+              if (!more || !w.active(i, c + 1)) mma_commit(elected, &sm.o_full[i]);
+              pph ^= 1u << i;
+              started[i] = true;
             }
-            __syncwarp();
-            started[i] = true;
+            if (more && w.active(i, c + 1)) product_s(i, sk, c + 1);
           }
-          if (more && active(i, c + 1)) {
-            if (!have_k) wait(&sm.kv_full[sk], ph);
-            have_k = true;
-            tc_fence_after();
-            product_s(i, sk);
+          mma_commit(elected, &sm.kv_empty[sv]);
+          if (more) {
+            mma_commit(elected, &sm.kv_empty[sk]);
+            rk.next();
           }
         }
-        if (lane == 0) {
-          mma_commit(&sm.kv_empty[sv]);
-          if (more) mma_commit(&sm.kv_empty[sk]);
-        }
-        __syncwarp();
-        if (more) next();
       }
-      if (lane == 0) mma_commit(&sm.fin);
-      __syncwarp();
+      mma_commit(elected, &sm.fin);
       if (!mbar_wait_slow(&sm.fin, 0, nullptr)) bad = true;
-    } else if (warp < kSoftWarps && (warp < 4 || two)) {
-      const int i = warp >> 2;
-      const int r = tid & (kTile - 1);
-      const int first = t0 + i * tile_tokens, last = min(first + tile_tokens, sp.n) - 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int i = warp >> 2;
+    const int r = tid & (kTile - 1);
+    const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + kColS + 128 * i, to = lanes + kColO + 128 * i;
+    uint32_t sph = 0, oph = 0;
+    Ring<kItems> ri;
+    Item it;
+    while (!bad && next_item(ri, &it)) {
+      const Walk w(it, a.window, tile_tokens);
+      if (i == 1 && !w.two) continue;
+      const Span& sp = w.sp;
+      const int first = it.t0 + i * tile_tokens, last = min(first + tile_tokens, it.n) - 1;
+      const int klo = i == 0 ? w.klo[0] : w.klo[1], khi = i == 0 ? w.khi[0] : w.khi[1];
       const int t = first + (r >> log_g);
-      const int head = (kv_head << log_g) + (r & ((1 << log_g) - 1));
-      const bool valid = t < sp.n;
+      const int head = (it.kv_head << log_g) + (r & ((1 << log_g) - 1));
+      const bool valid = t < it.n;
       const int lo = sp.lo(t), hi = sp.hi(t);  // (a row behind the last token: whatever it computes is dropped)
-      const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const uint32_t ts = lanes + kColS + 128 * i, to = lanes + kColO + 128 * i;
       const float slope2 = kBias ? __ldg(a.alibi_slopes + head) * 1.4426950408889634f : 0.0f;
       const float scale = kCap || kBias ? 1.0f : a.scale_log2;  // what is left to multiply by in the exponent
-      float m = -CUDART_INF_F, l = 0.0f;
+      float m = -CUDART_INF_F;
+      u64x l2[2] = {0ull, 0ull};  // the sum of p, in four parts
       bool started = false;
-      uint32_t sph = 0;
 #pragma unroll 1
-      for (int c = 0; c < steps; ++c) {
-        if (!active(i, c)) continue;
-        const int j0 = (top - 1 - c) * kTile;
+      for (int j = khi - 1; j >= klo; --j) {
+        const int j0 = j * kTile;
         if (!mbar_wait(&sm.s_full[i], sph, abort)) bad = true;
         sph ^= 1u;
         tc_fence_after();
@@ -567,96 +775,153 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s + 32 * x);
         tmem_wait_ld();
-        if (kCap) {
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = capped(s[e], a.softcap_exp, a.softcap);
-        }
+        if (kCap) cap_scores(s, a);
         if (kBias) {
           const float d0 = static_cast<float>(j0 - t);
+          if (j0 + kTile - 1 <= first) {  // no key behind a query: linear
+            const u64x k2 = kCap ? pk2(1.0f, 1.0f) : pk2(a.scale_log2, a.scale_log2);
+            const u64x sl = pk2(slope2, slope2), b2 = pk2(slope2 * d0, slope2 * d0);
 #pragma unroll
-          for (int e = 0; e < kTile; ++e)
-            s[e] = fmaf(-slope2, fabsf(d0 + static_cast<float>(e)), kCap ? s[e] : s[e] * a.scale_log2);
+            for (int e = 0; e < kTile; e += 2)
+              upk2(fma2(pk2(s[e], s[e + 1]), k2, fma2(pk2(static_cast<float>(e), static_cast<float>(e + 1)), sl, b2)),
+                   s[e], s[e + 1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kTile; ++e)
+              s[e] = fmaf(-slope2, fabsf(d0 + static_cast<float>(e)), kCap ? s[e] : s[e] * a.scale_log2);
+          }
         }
-        if (j0 + kTile > sp.hi(first) || j0 < sp.lo(last)) {
+        const bool masked = j0 + kTile > sp.hi(first) || j0 < sp.lo(last);
+        if (masked) {
           const int e0 = lo - j0, e1 = hi - j0;
 #pragma unroll
           for (int e = 0; e < kTile; ++e) s[e] = e >= e0 && e < e1 ? s[e] : -CUDART_INF_F;
         }
-        float mx = max3f(s[0], s[1], s[2]);
+        float mx4[4];  // four chains
 #pragma unroll
-        for (int e = 3; e < kTile - 1; e += 2) mx = max3f(mx, s[e], s[e + 1]);
-        mx = fmaxf(mx, s[kTile - 1]) * scale;
+        for (int x = 0; x < 4; ++x) mx4[x] = fmaxf(s[2 * x], s[2 * x + 1]);
+#pragma unroll
+        for (int e = 8; e < kTile; e += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mx4[x] = max3f(mx4[x], s[e + 2 * x], s[e + 2 * x + 1]);
+        const float mx = fmaxf(max3f(mx4[0], mx4[1], mx4[2]), mx4[3]) * scale;
         const bool moves = mx > m + kLazy || (m == -CUDART_INF_F && mx > m);
         if (__any_sync(0xffffffffu, moves)) {
           const float mn = moves ? mx : m;
           const float alpha = moves ? ex2(m - mn) : 1.0f;
           if (started) {  // O is at rest: the product before S is complete
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float o[32];
-              tmem_ld32(to + 32 * x, o);
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) {
+              float o[16];
+              tmem_ld16(to + 16 * x, o);
               tmem_wait_ld();
+              uint32_t v[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= alpha;
-              tmem_st32(to + 32 * x, o);
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * alpha);
+              tmem_st16(to + 16 * x, v);
             }
           }
-          l *= alpha;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) l2[x] = fma2(l2[x], pk2(alpha, alpha), 0ull);
           m = mn;
         }
         started = true;
         const float base = m == -CUDART_INF_F ? 0.0f : -m;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t w[16];
+        const u64x scale2 = pk2(scale, scale), base2 = pk2(base, base);
+        // P of 32 keys; of each 8 pairs poly go to the FMA pipe
+        auto exps = [&](int x, auto poly) {
+          uint32_t v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(fmaf(s[32 * x + 2 * e], scale, base));
-            const float p1 = ex2(fmaf(s[32 * x + 2 * e + 1], scale, base));
-            l += p0 + p1;
-            w[e] = pack2<kBF16>(p0, p1);
+            const u64x y = fma2(pk2(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), scale2, base2);
+            float p0, p1;
+            if ((e * poly.value) % 8 < poly.value) {
+              ex2_fma<kBF16>(y, p0, p1);
+            } else {
+              upk2(y, p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+            }
+            l2[e & 1] = add2(l2[e & 1], pk2(p0, p1));
+            v[e] = pack2<kBF16>(p0, p1);
           }
-          tmem_st16(ts + 16 * x, w);
+          tmem_st16(ts + 16 * x, v);
+        };
+        auto hand_over = [&](uint64_t* bar) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          if (masked) {
+            exps(x, std::integral_constant<int, 0>());
+            exps(x + 1, std::integral_constant<int, 0>());
+          } else {
+            exps(x, std::integral_constant<int, kCap || kBias ? POLYB : POLY>());
+            exps(x + 1, std::integral_constant<int, kCap || kBias ? POLYB : POLY>());
+          }
+          hand_over(x == 0 ? &sm.p_half[i] : &sm.p_full[i]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[i]);
       }
-      if (!mbar_wait(&sm.o_full[i], 0, abort)) bad = true;
+      if (!mbar_wait(&sm.o_full[i], oph, abort)) bad = true;
+      oph ^= 1u;
       tc_fence_after();
+      float l, l1;
+      upk2(add2(l2[0], l2[1]), l, l1);
+      l += l1;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      bool finite = true;
-      uint16_t* dst = a.out + (row0 + t) * a.out_stride + head * kHeadDim;
+      // 64 dims at a time: my row in 16 bits into the warp's staging rows,
+      // 16-byte piece x of row r at x ^ (r % 8); then the warp writes its 32
+      // rows, four at a time
+      uint8_t* stage = sm.out[warp];
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        bool finite = true;
+#pragma unroll 1
+        for (int x = 0; x < kHalf / 16; ++x) {
+          float o[16];
+          tmem_ld16(to + kHalf * hf + 16 * x, o);
+          tmem_wait_ld();
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        float o[32];
-        tmem_ld32(to + 32 * x, o);
-        tmem_wait_ld();
-        uint32_t w[16];
+          for (int e = 0; e < 2; ++e) {
+            uint32_t v[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          finite = finite && isfinite(o[2 * e]) && isfinite(o[2 * e + 1]);
-          w[e] = pack2<kBF16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+            for (int y = 0; y < 4; ++y) {
+              const float v0 = o[8 * e + 2 * y] * inv, v1 = o[8 * e + 2 * y + 1] * inv;
+              finite = finite && fabsf(v0) < CUDART_INF_F && fabsf(v1) < CUDART_INF_F;
+              v[y] = pack2<kBF16>(v0, v1);
+            }
+            *reinterpret_cast<uint4*>(stage + lane * kHeadDim + 16 * ((2 * x + e) ^ (lane & 7))) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
         }
-        if (valid) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4*>(dst)[4 * x + e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        __syncwarp();
+#pragma unroll 4
+        for (int x = 0; x < 8; ++x) {
+          const int wr = 4 * x + (lane >> 3), row = (warp & 3) * 32 + wr;
+          const int tr = first + (row >> log_g);
+          if (tr < it.n)
+            reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(it.row0 + tr) * a.out_stride +
+                                     ((it.kv_head << log_g) + (row & ((1 << log_g) - 1))) * kHeadDim +
+                                     kHalf * hf)[lane & 7] =
+                *reinterpret_cast<const uint4*>(stage + wr * kHeadDim + 16 * ((lane & 7) ^ (wr & 7)));
+        }
+        __syncwarp();
+        // rows that a masked value may have spoilt
+        uint32_t todo = __ballot_sync(0xffffffffu, valid && !finite && l > 0.0f && l < CUDART_INF_F);
+        while (todo != 0u) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1u;
+          const int tx = __shfl_sync(0xffffffffu, t, src), hx = __shfl_sync(0xffffffffu, head, src);
+          const float sx = __shfl_sync(0xffffffffu, slope2, src), mx = __shfl_sync(0xffffffffu, m, src);
+          const float lx = __shfl_sync(0xffffffffu, l, src);
+          fix_row<kBF16>(a, it.row0, tx, hx, it.kv_head, hf, klo * kTile, min(khi * kTile, a.n_tokens - it.row0),
+                         sp.lo(tx), sp.hi(tx), sx, mx, lx);
         }
       }
-      // rows that a masked value may have spoilt
-      __syncwarp();
-      uint32_t todo = __ballot_sync(0xffffffffu, valid && !finite && l > 0.0f && l < CUDART_INF_F);
-      while (todo != 0u) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1u;
-        const int ts_ = __shfl_sync(0xffffffffu, t, src), hs = __shfl_sync(0xffffffffu, head, src);
-        const float sl = __shfl_sync(0xffffffffu, slope2, src), ms = __shfl_sync(0xffffffffu, m, src);
-        const float ls = __shfl_sync(0xffffffffu, l, src);
-        const int k1 = static_cast<int>(min(static_cast<int64_t>(khi[i]) * kTile, a.n_tokens - row0));
-        fix_row<kBF16>(a, row0, ts_, hs, kv_head, klo[i] * kTile, k1, sp.lo(ts_), sp.hi(ts_), sl, ms, ls);
-      }
+      tc_fence_before();  // O is read: orders the next item's first P, which lets the products write it again
     }
   }
   if (bad) record_status(a.status, KVQ_ERR_DEVICE_TIMEOUT);
@@ -713,9 +978,11 @@ template <bool kBF16, bool kCap, bool kBias>
 cudaError_t launch_one(const PrefillArgs& a, cudaStream_t stream) {
   const cudaError_t e = ensure_smem_limit<prefill_kernel<kBF16, kCap, kBias>>(kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int64_t items = (static_cast<int64_t>(a.n_tokens) >> (8 - a.log_group)) + a.batch;
-  return launch_pdl(prefill_kernel<kBF16, kCap, kBias>, dim3(static_cast<unsigned>(items * a.num_kv_heads)),
-                    dim3(kThreads), kSmemBytes, stream, a);
+  // the most items that these rows can make, or a CTA per multiprocessor
+  const int64_t items = ((static_cast<int64_t>(a.n_tokens) >> (8 - a.log_group)) + a.batch) * a.num_kv_heads;
+  const int64_t ctas = std::min<int64_t>(items, device_sm_count());
+  return launch_pdl(prefill_kernel<kBF16, kCap, kBias>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmemBytes,
+                    stream, a);
 }
 template <bool kBF16>
 cudaError_t launch_type(const PrefillArgs& a, cudaStream_t stream) {

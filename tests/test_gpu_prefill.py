@@ -154,6 +154,8 @@ def test_large_scores_and_saturated_caps(kvq, cuda):
     _run(kvq, [600, 40], 4, 2, "bf16", mutate=louder)
     _run(kvq, [600, 40], 4, 2, "bf16", mutate=louder, softcap=2.0)
     _run(kvq, [600, 40], 4, 2, "bf16", softcap=3e5)
+    _run(kvq, [300], 4, 2, "fp16", softcap=1e-3, softmax_scale=20.0)
+    _run(kvq, [300], 4, 2, "fp16", softcap=9.0)  # most rows below half of it, below it, some beyond
 
 
 def test_rising_scores_move_the_maximum(kvq, cuda):
