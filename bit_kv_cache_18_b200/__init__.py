@@ -67,6 +67,8 @@ class ScoreOpts(ctypes.Structure):
 def lib():
     """Load libkvq.so (raises if it is absent: there is no other path)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -326,38 +328,63 @@ def kvq_decode_attention_window(pool, num_blocks, num_kv_heads, window, sink, re
 
 
 # ---- a serving step around the cache --------------------------------------------
+# These calls are short on the device (a few microseconds for a decode step), so
+# their checks are kept to a handful of attribute reads, without generators,
+# imports or formatted messages on the way of a call that is right.
 
-def _require(ok: bool, what: str):
+_torch = None
+_codes = {}
+
+
+def _need_torch():
+    global _torch, _codes
+    if _torch is None:
+        import torch
+        _codes = {torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16, torch.float32: KVQ_F32}
+        _torch = torch
+    return _torch
+
+
+def _refuse(what: str, why: str):
     """Argument rules that only the tensors show (shape, type, layout, device):
     refused like the library's own, before anything is launched."""
-    if not ok:
-        raise KvqError(KVQ_ERR_INVALID, what)
+    raise KvqError(KVQ_ERR_INVALID, f"{what}: {why}")
 
 
-def _require_on_device(what: str, *tensors):
-    """Every tensor on the current CUDA device, where the launch goes."""
-    import torch
-    dev = torch.cuda.current_device()
-    _require(all(t is None or (t.is_cuda and t.device.index == dev) for t in tensors),
-             f"{what}: a tensor is not on the current CUDA device")
+def _on_device(what: str, *tensors) -> int:
+    """The current CUDA device, where the launch goes and every tensor has to be."""
+    dev = (_torch or _need_torch()).cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse(what, "a tensor is not on the current CUDA device")
+    return dev
 
 
-def _require_int32(what: str, *tensors):
-    import torch
-    _require(all(t is None or (t.dtype == torch.int32 and t.is_contiguous()) for t in tensors),
-             f"{what}: tables and lengths are contiguous int32 tensors")
+def _all_int32(what: str, *tensors):
+    i32 = _torch.int32
+    for t in tensors:
+        if t is not None and not (t.dtype is i32 and t.is_contiguous()):
+            _refuse(what, "tables and lengths are contiguous int32 tensors")
 
 
-def _require_rows(what: str, *tensors):
-    """[n, heads, 128] with contiguous rows."""
-    _require(all(t is None or (t.dim() == 3 and t.shape[2] == HEAD_DIM and
-                               (t.numel() == 0 or (t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == HEAD_DIM))))
-                 for t in tensors), f"{what}: rows are [tokens, heads, {HEAD_DIM}] with contiguous heads")
+def _rows(what: str, t):
+    """[n, heads, 128] with contiguous heads -> n, heads, elements from one
+    token's row to the next (any value does for a single row)."""
+    if t.dim() != 3:
+        _refuse(what, "rows are [tokens, heads, 128]")
+    n, heads, d = t.shape
+    st = t.stride()
+    if d != HEAD_DIM or (n * heads > 0 and (st[2] != 1 or (heads > 1 and st[1] != HEAD_DIM))):
+        _refuse(what, "rows are [tokens, heads, 128] with contiguous heads")
+    return n, heads, st[0] if n > 1 else heads * HEAD_DIM
 
 
-def _row_stride(t) -> int:
-    """Elements from one token's row to the next (any value does for a single row)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream_of(stream, dev: int):
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def kvq_update_tables(ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens, positions,
@@ -367,19 +394,19 @@ def kvq_update_tables(ring, state_in, state_out, seq_lens, target_lens, lens_out
     target_lens and lens_out [batch], block_table [batch, max_blocks],
     cu_seqlens [batch + 1], positions, seq_ids and slots [max_tokens]."""
     what = "kvq_update_tables"
+    every = (ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens, positions, seq_ids,
+             slots)
+    dev = _on_device(what, *every)
+    _all_int32(what, *every)
     batch, n = seq_lens.numel(), positions.numel()
-    _require_on_device(what, ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens,
-                       positions, seq_ids, slots)
-    _require_int32(what, ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens,
-                   positions, seq_ids, slots)
-    _require(state_in.numel() >= 4 and state_out.numel() >= 4 and target_lens.numel() == batch and
-             lens_out.numel() == batch and block_table.dim() == 2 and block_table.shape[0] == batch and
-             cu_seqlens.numel() == batch + 1 and seq_ids.numel() == n and slots.numel() == n,
-             f"{what}: buffer sizes")
-    rc = lib().kvq_update_tables(_ptr(ring), ring.numel(), _ptr(state_in), _ptr(state_out), _ptr(seq_lens),
-                                 _ptr(target_lens), _ptr(lens_out), batch, _ptr(block_table), block_table.shape[1],
-                                 _ptr(cu_seqlens), n, _ptr(positions), _ptr(seq_ids), _ptr(slots),
-                                 _stream_ptr(stream))
+    if not (state_in.numel() >= 4 and state_out.numel() >= 4 and target_lens.numel() == batch and
+            lens_out.numel() == batch and block_table.dim() == 2 and block_table.shape[0] == batch and
+            cu_seqlens.numel() == batch + 1 and seq_ids.numel() == n and slots.numel() == n):
+        _refuse(what, "buffer sizes")
+    rc = lib().kvq_update_tables(ring.data_ptr(), ring.numel(), state_in.data_ptr(), state_out.data_ptr(),
+                                 seq_lens.data_ptr(), target_lens.data_ptr(), lens_out.data_ptr(), batch,
+                                 block_table.data_ptr(), block_table.shape[1], cu_seqlens.data_ptr(), n,
+                                 positions.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(), _stream_of(stream, dev))
     _check(rc, what)
 
 
@@ -388,7 +415,8 @@ ROPE_SCALINGS = ("none", "linear", "ntk", "bands", "yarn")
 
 def make_rope(rotary_dim=HEAD_DIM, base=10000.0, interleaved=False, scaling="none", factor=1.0, original_len=0,
               low=0.0, high=0.0) -> RopeDesc:
-    _require(scaling in ROPE_SCALINGS, "make_rope: scaling")
+    if scaling not in ROPE_SCALINGS:
+        _refuse("make_rope", "scaling")
     return RopeDesc(rotary_dim, int(interleaved), ROPE_SCALINGS.index(scaling), original_len, base, factor, low, high)
 
 
@@ -412,42 +440,55 @@ def new_rope_table(desc: RopeDesc, device="cuda"):
 def kvq_rope(desc, table, magnitude, positions, q, k=None, q_out=None, k_out=None, stream=None):
     """Rotate q [n, Hq, 128] and k [n, Hkv, 128] (fp16 or bf16) by positions
     (int32 [n]) into q_out and k_out, in place where those are None."""
-    import torch
     what = "kvq_rope"
-    q_out = q if q_out is None else q_out
-    k_out = k if k_out is None else k_out
-    _require((k is None) == (k_out is None), f"{what}: k_out without k")
-    n = positions.numel()
-    _require_on_device(what, table, positions, q, k, q_out, k_out)
-    _require_int32(what, positions)
-    _require_rows(what, q, k, q_out, k_out)
-    _require(table.dtype == torch.int64 and table.is_contiguous() and table.numel() == desc.rotary_dim // 2,
-             f"{what}: a table of another descriptor")
-    _require(q.shape[0] == n and q_out.shape == q.shape and q_out.dtype == q.dtype and
-             (k is None or (k.shape[0] == n and k_out.shape == k.shape and k.dtype == k_out.dtype == q.dtype)),
-             f"{what}: shapes and types")
-    hk = 0 if k is None else k.shape[1]
-    rc = lib().kvq_rope(ctypes.byref(desc), _ptr(table), magnitude, _ptr(positions), n, _ptr(q), _row_stride(q),
-                        _ptr(q_out), _row_stride(q_out), q.shape[1], _ptr(k), _row_stride(k) if hk else 0,
-                        _ptr(k_out), _row_stride(k_out) if hk else 0, hk, _dtype_code(q), _stream_ptr(stream))
+    if k is None and k_out is not None:
+        _refuse(what, "k_out without k")
+    dev = _on_device(what, table, positions, q, k, q_out, k_out)
+    _all_int32(what, positions)
+    if not (table.dtype is _torch.int64 and table.is_contiguous() and table.numel() == desc.rotary_dim // 2):
+        _refuse(what, "a table of another descriptor")
+    n, dtype = positions.numel(), q.dtype
+    nq, hq, qs = _rows(what, q)
+    qos, hk, ks, kos = qs, 0, 0, 0
+    ok = nq == n and dtype in _codes
+    if q_out is None:
+        q_out = q
+    else:
+        no, ho, qos = _rows(what, q_out)
+        ok = ok and no == n and ho == hq and q_out.dtype is dtype
+    if k is not None:
+        nk, hk, ks = _rows(what, k)
+        kos = ks
+        ok = ok and nk == n and k.dtype is dtype
+        if k_out is None:
+            k_out = k
+        else:
+            no, ho, kos = _rows(what, k_out)
+            ok = ok and no == n and ho == hk and k_out.dtype is dtype
+    if not ok:
+        _refuse(what, "shapes and types")
+    rc = lib().kvq_rope(ctypes.byref(desc), table.data_ptr(), magnitude, positions.data_ptr(), n, q.data_ptr(), qs,
+                        q_out.data_ptr(), qos, hq, _addr(k), ks, _addr(k_out), kos, hk, _codes[dtype],
+                        _stream_of(stream, dev))
     _check(rc, what)
 
 
 def make_score_opts(softmax_scale=0.0, softcap=0.0, window=0, alibi_slopes=None) -> ScoreOpts:
     """alibi_slopes: fp32 device tensor [num_q_heads], kept alive by the options."""
-    import torch
     if alibi_slopes is not None:
-        _require(alibi_slopes.is_cuda and alibi_slopes.dtype == torch.float32 and alibi_slopes.is_contiguous(),
-                 "make_score_opts: alibi_slopes is a contiguous fp32 device tensor")
-    o = ScoreOpts(softmax_scale, softcap, window, alibi_slopes.data_ptr() if alibi_slopes is not None else None)
+        if not (alibi_slopes.is_cuda and alibi_slopes.dtype is _need_torch().float32 and alibi_slopes.is_contiguous()):
+            _refuse("make_score_opts", "alibi_slopes is a contiguous fp32 device tensor")
+    o = ScoreOpts(softmax_scale, softcap, window, _addr(alibi_slopes))
     o.slopes_tensor = alibi_slopes
     return o
 
 
-def _require_opts(what: str, opts, num_q_heads: int):
+def _slopes_of(what: str, opts, num_q_heads: int):
+    """The options' slopes (None without), one per query head."""
     slopes = getattr(opts, "slopes_tensor", None)
-    _require_on_device(what, slopes)
-    _require(slopes is None or slopes.numel() == num_q_heads, f"{what}: one slope per query head")
+    if slopes is not None and slopes.numel() != num_q_heads:
+        _refuse(what, "one slope per query head")
+    return slopes
 
 
 def kvq_prefill_attention(q, k, v, cu_seqlens, out, opts=None, prefix_lens=None, stream=None):
@@ -456,19 +497,19 @@ def kvq_prefill_attention(q, k, v, cu_seqlens, out, opts=None, prefix_lens=None,
     cu_seqlens int32 [batch + 1], prefix_lens int32 [batch] or None, opts from
     make_score_opts."""
     what = "kvq_prefill_attention"
-    batch = cu_seqlens.numel() - 1
-    _require_on_device(what, q, k, v, out, cu_seqlens, prefix_lens)
-    _require_int32(what, cu_seqlens, prefix_lens)
-    _require_rows(what, q, k, v, out)
-    _require(batch >= 0 and out.shape == q.shape and k.shape == v.shape and k.shape[0] == q.shape[0] and
-             q.dtype == k.dtype == v.dtype == out.dtype and (prefix_lens is None or prefix_lens.numel() == batch),
-             f"{what}: shapes and types")
-    if opts is not None:
-        _require_opts(what, opts, q.shape[1])
-    rc = lib().kvq_prefill_attention(ctypes.byref(opts) if opts is not None else None, _ptr(q), _row_stride(q),
-                                     _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), _ptr(out), _row_stride(out),
-                                     q.shape[0], q.shape[1], k.shape[1], _ptr(cu_seqlens), batch, _ptr(prefix_lens),
-                                     _dtype_code(q), _stream_ptr(stream))
+    nq, hq, qs = _rows(what, q)
+    dev = _on_device(what, q, k, v, out, cu_seqlens, prefix_lens, _slopes_of(what, opts, hq))
+    _all_int32(what, cu_seqlens, prefix_lens)
+    nk, hk, ks = _rows(what, k)
+    nv, hv, vs = _rows(what, v)
+    no, ho, os_ = _rows(what, out)
+    batch, dtype = cu_seqlens.numel() - 1, q.dtype
+    if not (batch >= 0 and nq == nk == nv == no and ho == hq and hv == hk and dtype in _codes and k.dtype is dtype and
+            v.dtype is dtype and out.dtype is dtype and (prefix_lens is None or prefix_lens.numel() == batch)):
+        _refuse(what, "shapes and types")
+    rc = lib().kvq_prefill_attention(ctypes.byref(opts) if opts is not None else None, q.data_ptr(), qs, k.data_ptr(),
+                                     ks, v.data_ptr(), vs, out.data_ptr(), os_, nq, hq, hk, cu_seqlens.data_ptr(),
+                                     batch, _addr(prefix_lens), _codes[dtype], _stream_of(stream, dev))
     _check(rc, what)
 
 
@@ -488,23 +529,28 @@ def new_scored_workspace(num_blocks, num_kv_heads, batch, num_q_heads, max_seq_l
 
 
 def kvq_decode_attention_scored(pool, num_blocks, num_kv_heads, q, block_table, seq_lens, max_seq_len, out, workspace,
-                                opts, stream=None, preset=(4, 2)):
+                                opts=None, stream=None, preset=(4, 2)):
     """kvq_decode_attention with score options (make_score_opts); workspace
     from new_scored_workspace() with the same window."""
     what = "kvq_decode_attention_scored"
     desc = make_desc(num_blocks, num_kv_heads, pool, preset)
+    if q.dim() != 3:
+        _refuse(what, "q is [batch, heads, 128]")
     batch, hq, d = q.shape
-    _require_on_device(what, pool, q, block_table, seq_lens, out, workspace)
-    _require_int32(what, block_table, seq_lens)
-    _require(d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape and
-             block_table.dim() == 2 and block_table.shape[0] == batch and seq_lens.numel() == batch,
-             f"{what}: shapes and layout")
-    _require(pool.numel() * pool.element_size() >= kvq_cache_bytes(desc), f"{what}: pool too small")
-    _require_opts(what, opts, hq)
-    rc = lib().kvq_decode_attention_scored(ctypes.byref(desc), ctypes.byref(opts), _ptr(q), _dtype_code(q), batch, hq,
-                                           _ptr(block_table), block_table.shape[1], _ptr(seq_lens), max_seq_len,
-                                           _ptr(out), _dtype_code(out), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    dev = _on_device(what, pool, q, block_table, seq_lens, out, workspace, _slopes_of(what, opts, hq))
+    _all_int32(what, block_table, seq_lens)
+    if not (d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape and
+            q.dtype in _codes and out.dtype in _codes and block_table.dim() == 2 and block_table.shape[0] == batch and
+            seq_lens.numel() == batch and workspace.is_contiguous()):
+        _refuse(what, "shapes, types and layout")
+    # (a pool of an unsupported preset has no size: the library refuses it below)
+    if not pool.is_contiguous() or pool.numel() * pool.element_size() < lib().kvq_cache_bytes(ctypes.byref(desc)):
+        _refuse(what, "pool too small")
+    rc = lib().kvq_decode_attention_scored(ctypes.byref(desc), ctypes.byref(opts) if opts is not None else None,
+                                           q.data_ptr(), _codes[q.dtype], batch, hq, block_table.data_ptr(),
+                                           block_table.shape[1], seq_lens.data_ptr(), max_seq_len, out.data_ptr(),
+                                           _codes[out.dtype], workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(), _stream_of(stream, dev))
     _check(rc, what)
 
 

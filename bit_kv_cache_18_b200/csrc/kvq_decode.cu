@@ -819,15 +819,23 @@ __device__ __forceinline__ void window_part(const DecodeArgs& a, uint8_t* smem) 
 // Score options (kvq_score_opts): the base-2 score s of a token `dist`
 // positions before the newest becomes
 //   cap tanh(s / cap) - slope dist,
-// cap and slope in base-2 units too.  tanh(x) = 1 - 2 / (e^2x + 1) keeps an
-// absolute error of about 2^-22 cap in the score (e^2x = 0 and infinity give
-// -cap and cap), where the hardware's tanh approximation (2^-11) would cost a
-// softcap of 50 two percent of every probability.
+// cap and slope in base-2 units too.  Up to |s| = cap / 2, s T(s^2) with T the
+// interpolation of tanh(sqrt u) / sqrt u at the four Chebyshev points of [0,
+// 1/4], its coefficients in units of the cap: off by 5.5e-7 of itself, so
+// right for caps of any size, and without the exponential and reciprocal of
+// the other form, cap (1 - 2 / (e^2x + 1)) (e^2x = 0 and infinity give -cap and
+// cap; off by 2^-22 cap, where the hardware's tanh, 2^-11, would cost a softcap
+// of 50 two percent of every probability).
 __device__ __forceinline__ float scored(const DecodeArgs& a, float s, float slope, float dist) {
   if (a.softcap > 0.0f) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * a.softcap_exp) + 1.0f));
-    s = fmaf(-2.0f * a.softcap, r, a.softcap);
+    if (fabsf(s) <= a.softcap_near) {
+      const float u = s * s;
+      s *= fmaf(fmaf(fmaf(a.softcap_coef[2], u, a.softcap_coef[1]), u, a.softcap_coef[0]), u, 0.99999945f);
+    } else {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * a.softcap_exp) + 1.0f));
+      s = fmaf(-2.0f * a.softcap, r, a.softcap);
+    }
   }
   return fmaf(-slope, dist, s);
 }

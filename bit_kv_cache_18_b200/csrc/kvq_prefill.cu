@@ -40,16 +40,9 @@
 #include <math_constants.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "kvq_internal.cuh"
 
-#ifndef POLY
-#define POLY 2
-#endif
-#ifndef POLYB
-#define POLYB 0
-#endif
 namespace kvq {
 namespace {
 
@@ -253,6 +246,13 @@ __device__ __forceinline__ u64x pk2(float a, float b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
+// The same value twice, in registers that stay: from a plain constant the
+// compiler makes the pair anew, two moves, at every use.
+__device__ __forceinline__ u64x twice(float a) {
+  u64x r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
+  return r;
+}
 __device__ __forceinline__ void upk2(u64x v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
@@ -270,36 +270,6 @@ __device__ __forceinline__ u64x fma2(u64x a, u64x b, u64x c) {
   u64x d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
-}
-// 2^x of two x <= kLazy on the FMA pipe: x = n + f with n the nearest integer,
-// 2^f by interpolation at the Chebyshev points of [-1/2, 1/2], n added to the
-// exponent.  Degree 3 is off by 1.0e-4, 1/20 of the half step of bf16, degree
-// 4 by 3.5e-6, 1/70 of that of fp16.  An x below -126 gives 2^-126, so masked
-// places do not come here.
-template <bool kBF16>
-__device__ __forceinline__ void ex2_fma(u64x x, float& p0, float& p1) {
-  auto c = [](float v) { return pk2(v, v); };
-  float x0, x1;
-  upk2(x, x0, x1);
-  x = pk2(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
-  const u64x t = add2(x, c(12582912.0f));  // 1.5 * 2^23: the low bits hold n
-  const u64x f = fma2(add2(t, c(-12582912.0f)), c(-1.0f), x);
-  u64x p;
-  if (kBF16) {
-    p = fma2(c(0.0558382829f), f, c(0.2426394785f));
-    p = fma2(p, f, c(0.6931367338f));
-    p = fma2(p, f, c(0.9999245570f));
-  } else {
-    p = fma2(c(0.0096663685f), f, c(0.0559219758f));
-    p = fma2(p, f, c(0.2402234904f));
-    p = fma2(p, f, c(0.6931210452f));
-    p = fma2(p, f, c(1.0f));
-  }
-  float a, b, n0, n1;
-  upk2(p, a, b);
-  upk2(t, n0, n1);
-  p0 = __int_as_float(__float_as_int(a) + (__float_as_int(n0) << 23));
-  p1 = __int_as_float(__float_as_int(b) + (__float_as_int(n1) << 23));
 }
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
@@ -337,12 +307,15 @@ __device__ __forceinline__ float capped_far(float d, const PrefillArgs& a) {
 }
 template <int kN>
 __device__ __forceinline__ void capped_near(float (&s)[kTile], const float (&coef)[kN]) {
+  u64x c[kN];
+#pragma unroll
+  for (int x = 0; x < kN; ++x) c[x] = twice(coef[x]);
 #pragma unroll
   for (int e = 0; e < kTile; e += 2) {
     const u64x d = pk2(s[e], s[e + 1]), u = mul2(d, d);
-    u64x p = pk2(coef[kN - 1], coef[kN - 1]);
+    u64x p = c[kN - 1];
 #pragma unroll
-    for (int x = kN - 2; x >= 0; --x) p = fma2(p, u, pk2(coef[x], coef[x]));
+    for (int x = kN - 2; x >= 0; --x) p = fma2(p, u, c[x]);
     upk2(mul2(d, p), s[e], s[e + 1]);
   }
 }
@@ -779,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (kBias) {
           const float d0 = static_cast<float>(j0 - t);
           if (j0 + kTile - 1 <= first) {  // no key behind a query: linear
-            const u64x k2 = kCap ? pk2(1.0f, 1.0f) : pk2(a.scale_log2, a.scale_log2);
-            const u64x sl = pk2(slope2, slope2), b2 = pk2(slope2 * d0, slope2 * d0);
+            const u64x k2 = twice(kCap ? 1.0f : a.scale_log2);
+            const u64x sl = twice(slope2), b2 = twice(slope2 * d0);
 #pragma unroll
             for (int e = 0; e < kTile; e += 2)
               upk2(fma2(pk2(s[e], s[e + 1]), k2, fma2(pk2(static_cast<float>(e), static_cast<float>(e + 1)), sl, b2)),
@@ -827,25 +800,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         started = true;
         const float base = m == -CUDART_INF_F ? 0.0f : -m;
-        const u64x scale2 = pk2(scale, scale), base2 = pk2(base, base);
-        // P of 32 keys; of each 8 pairs poly go to the FMA pipe
-        auto exps = [&](int x, auto poly) {
-          uint32_t v[16];
+        const u64x scale2 = twice(scale), base2 = twice(base);
+        // P of 32 keys
+        auto exps = [&](int x, uint32_t (&v)[16]) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const u64x y = fma2(pk2(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), scale2, base2);
             float p0, p1;
-            if ((e * poly.value) % 8 < poly.value) {
-              ex2_fma<kBF16>(y, p0, p1);
-            } else {
-              upk2(y, p0, p1);
-              p0 = ex2(p0);
-              p1 = ex2(p1);
-            }
+            upk2(fma2(pk2(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), scale2, base2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
             l2[e & 1] = add2(l2[e & 1], pk2(p0, p1));
             v[e] = pack2<kBF16>(p0, p1);
           }
-          tmem_st16(ts + 16 * x, v);
         };
         auto hand_over = [&](uint64_t* bar) {
           tmem_wait_st();
@@ -853,17 +819,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           __syncwarp();
           if (lane == 0) mbar_arrive(bar);
         };
-#pragma unroll
-        for (int x = 0; x < 4; x += 2) {
-          if (masked) {
-            exps(x, std::integral_constant<int, 0>());
-            exps(x + 1, std::integral_constant<int, 0>());
-          } else {
-            exps(x, std::integral_constant<int, kCap || kBias ? POLYB : POLY>());
-            exps(x + 1, std::integral_constant<int, kCap || kBias ? POLYB : POLY>());
-          }
-          hand_over(x == 0 ? &sm.p_half[i] : &sm.p_full[i]);
-        }
+        uint32_t v[16];
+        exps(0, v);
+        tmem_st16(ts, v);
+        exps(1, v);
+        tmem_st16(ts + 16, v);
+        hand_over(&sm.p_half[i]);
+        exps(2, v);
+        tmem_st16(ts + 32, v);
+        exps(3, v);
+        tmem_st16(ts + 48, v);
+        hand_over(&sm.p_full[i]);
       }
       if (!mbar_wait(&sm.o_full[i], oph, abort)) bad = true;
       oph ^= 1u;

@@ -133,6 +133,12 @@ def test_large_scores_saturate_the_cap(kvq, cuda):
     _run(kvq, _wl([500, 33], 16, 2, 91), q_mul=200.0, softcap=2.0)
 
 
+@pytest.mark.parametrize("softcap", [1e-3, 6.0, 1e5])
+def test_caps_of_any_size(kvq, cuda, softcap):
+    """Tiny, around the scores (both forms of the cap in one row), huge (no cap in effect)."""
+    _run(kvq, _wl([500, 33], 16, 2, 96), softcap=softcap)
+
+
 def test_steep_and_zero_and_growing_biases(kvq, cuda):
     """A slope that leaves the newest token alone, a slope of zero, one that favours distant tokens."""
     _run(kvq, _wl([900, 33], 8, 1, 92), alibi_slopes=[100.0, 0.0, -0.01, 1e-6, 3.0, 1e30, 0.5, 0.01])
