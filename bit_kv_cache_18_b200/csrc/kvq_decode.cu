@@ -151,7 +151,7 @@ struct __align__(1024) Smem {
   int32_t tbl[kTblBlocks];                   // the split's block ids, -1 where absent (outside the split,
                                              // the sequence or the pool)
   float2 hq[8];                              // per head: sum(q~), max|q~|
-  float slope[8];                            // per head: distance bias per position, base 2 (score options)
+  alignas(16) float slope[8];                // per head: minus the distance bias per position, base 2 (score options)
   float red[R::kSoft][8][2];                 // cross-warp reductions
   float palpha[R::kSoft][8];                 // per softmax warp: factor of the pending O buffer
   float c1;                                  // max|q~| / 127: the unit of the query digits
@@ -819,25 +819,21 @@ __device__ __forceinline__ void window_part(const DecodeArgs& a, uint8_t* smem) 
 // Score options (kvq_score_opts): the base-2 score s of a token `dist`
 // positions before the newest becomes
 //   cap tanh(s / cap) - slope dist,
-// cap and slope in base-2 units too.  Up to |s| = cap / 2, s T(s^2) with T the
+// cap and slope in base-2 units too.  tanh(x) = 1 - 2 / (e^2x + 1) (e^2x = 0 and
+// infinity give -1 and 1) is off by 2^-22 of the cap, where the hardware's tanh,
+// 2^-11, would cost a softcap of 50 two percent of every probability; the two
+// MUFU operations hide behind the chunk's other work.  Caps for which that is
+// not enough (softcap_near > 0) take, up to |s| = cap / 2, s T(s^2) with T the
 // interpolation of tanh(sqrt u) / sqrt u at the four Chebyshev points of [0,
-// 1/4], its coefficients in units of the cap: off by 5.5e-7 of itself, so
-// right for caps of any size, and without the exponential and reciprocal of
-// the other form, cap (1 - 2 / (e^2x + 1)) (e^2x = 0 and infinity give -cap and
-// cap; off by 2^-22 cap, where the hardware's tanh, 2^-11, would cost a softcap
-// of 50 two percent of every probability).
-__device__ __forceinline__ float scored(const DecodeArgs& a, float s, float slope, float dist) {
-  if (a.softcap > 0.0f) {
-    if (fabsf(s) <= a.softcap_near) {
-      const float u = s * s;
-      s *= fmaf(fmaf(fmaf(a.softcap_coef[2], u, a.softcap_coef[1]), u, a.softcap_coef[0]), u, 0.99999945f);
-    } else {
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * a.softcap_exp) + 1.0f));
-      s = fmaf(-2.0f * a.softcap, r, a.softcap);
-    }
+// 1/4]: off by 5.5e-7 of the score itself.
+__device__ __forceinline__ float capped(const DecodeArgs& a, float s, bool large) {
+  if (large && fabsf(s) <= a.softcap_near) {
+    const float u = s * s;
+    return s * fmaf(fmaf(fmaf(a.softcap_coef[2], u, a.softcap_coef[1]), u, a.softcap_coef[0]), u, 0.99999945f);
   }
-  return fmaf(-slope, dist, s);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * a.softcap_exp) + 1.0f));
+  return fmaf(-2.0f * a.softcap, r, a.softcap);
 }
 
 // kWin: the instantiation that takes a bf16 window (a.win set); kScore: the
@@ -971,10 +967,12 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   // of the row goes to shared memory in the set-up below, cut to the split
   // and the pool.
   // With a sliding window the first split starts at the first block that holds
-  // a position of the window.  The score options walk the chunks from the
-  // newest to the oldest, since a distance bias makes scores fall with the
-  // distance: the running max is then found at once instead of moving with
-  // every chunk.
+  // a position of the window.  A distance bias makes scores fall with the
+  // distance, so with one the chunks are walked from the newest to the oldest:
+  // the running max is then found at once instead of moving with every chunk.
+  // (Either way the first chunks' blocks are known only with the length.)
+  const bool newest_first = kScore && a.alibi_slopes != nullptr;
+  const bool early = !kScore || (a.score_window == 0 && !newest_first);
   int blk0 = split * a.blocks_per_split;
   if constexpr (kScore) {
     if (a.score_window > 0) {
@@ -985,7 +983,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   const int32_t* bt_row = a.block_table + static_cast<int64_t>(b) * a.max_blocks_per_seq;
   constexpr int kTblPer = kTblBlocks / (32 * kLoadWarps);
   int32_t bfirst[kNV];  // loaders, lanes sg < kSegs: block ids of chunks 0 .. 2
-  if (!kScore && is_loader) {
+  if (early && is_loader) {
     const int nload = min(a.blocks_per_split, a.max_blocks_per_seq - blk0);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -1019,7 +1017,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   auto needed = [&](int blk) { return blk * kBlockSize < qhi && (blk + 1) * kBlockSize > qlo; };
   const int nchunks = blk1 > blk0 ? (blk1 - blk0 + kChunkBlocks - 1) / kChunkBlocks : 0;
   // the chunk of the split that is walked c-th
-  auto chunk_of = [&](int c) { return kScore ? nchunks - 1 - c : c; };
+  auto chunk_of = [&](int c) { return newest_first ? nchunks - 1 - c : c; };
   bool bad = false;      // a wait ran out: the results are void, the control flow is kept
   bool bad_blk = false;  // a block-table entry outside the pool (its tokens are skipped)
 
@@ -1053,7 +1051,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
   if (is_loader) {
     // my block ids of chunks 0 .. 2, cut to the split and the pool
     const int nblk = blk1 - blk0;
-    if constexpr (kScore) {  // the last chunks: known only with the length
+    if (!early) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
         const int j = kChunkBlocks * chunk_of(i) + seg_of<kWide>(warp, lane % kSegs);
@@ -1062,7 +1060,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
       }
     }
 #pragma unroll
-    for (int i = 0; !kScore && i < kNV; ++i) {
+    for (int i = 0; early && i < kNV; ++i) {
       const int j = kChunkBlocks * i + seg_of<kWide>(warp, lane % kSegs);
       if (!(j < nblk && needed(blk0 + j) && bfirst[i] >= 0 && bfirst[i] < a.num_blocks)) bfirst[i] = -1;
     }
@@ -1111,7 +1109,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
     const float inv = mx > 0.0f ? 127.0f / mx : 0.0f;
     if (st == 0) sm.c1 = mx * (1.0f / 127.0f);
     if (kScore && st < G)
-      sm.slope[st] = a.alibi_slopes != nullptr ? __ldg(a.alibi_slopes + h * G + st) * 1.4426950408889634f : 0.0f;
+      sm.slope[st] = a.alibi_slopes != nullptr ? __ldg(a.alibi_slopes + h * G + st) * -1.4426950408889634f : 0.0f;
 #pragma unroll
     for (int i = 0; i < kQHeads; ++i) {
       const int g = sw + kSoftWarps * i;
@@ -1427,38 +1425,60 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
       pick_digits(sr, sr2, d0, d1, d2);
       float dg[kHeads];
       float dmax = -CUDART_INF_F;
-      // (kScore) positions from my token to the newest, and the score of my
-      // g-th head without the running max
-      const float dist = static_cast<float>(L - 1 - (blk0 * kBlockSize + kChunkTokens * chunk_of(c) + stok));
-      auto score_of = [&](int g) {
-        const int e12 = static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]);
-        const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[g]));
-        return scored(a, fmaf(mt.x, xg, mt.y * qs[g]), sm.slope[hb + g], dist);
-      };
-      if constexpr (kScore) {
+      // the scores of my heads, less sub[g]; (kScore) with the options, dist the
+      // positions from my token to the newest
+      const float dist = kScore ? static_cast<float>(L - 1 - (blk0 * kBlockSize + kChunkTokens * chunk_of(c) + stok)) : 0.0f;
+      // form: 0 no softcap, 1 a softcap, 2 a large one
+      auto scores_as = [&](int form, const float (&sub)[kHeads], float (&out)[kHeads]) {
+        if (kHeads == 1) {
+          const int e12 = static_cast<int>(d1[0]) * 254 + static_cast<int>(d2[0]);
+          const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[0]));
+          if (kScore) {
+            float v = fmaf(mt.x, xg, mt.y * qs[0]);
+            if (form > 0) v = capped(a, v, form == 2);
+            out[0] = fmaf(sm.slope[hb], dist, v) - sub[0];
+          } else {
+            out[0] = fmaf(mt.x, xg, fmaf(mt.y, qs[0], -sub[0]));
+          }
+        } else {
+          const u64x mx2 = pk2(mt.x, mt.x), my2 = pk2(mt.y, mt.y);
+          const u64x k2 = pk2(1.0f / 64516.0f, 1.0f / 64516.0f), m2 = pk2(-12582912.0f, -12582912.0f);
 #pragma unroll
-        for (int g = 0; g < kHeads; ++g) {
-          dg[g] = score_of(g) - mr[g];
-          dmax = fmaxf(dmax, dg[g]);
+          for (int g = 0; g < (kHeads > 1 ? kHeads : 2); g += 2) {
+            const float xe0 = __int2float_rn(static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]));
+            const float xe1 = __int2float_rn(static_cast<int>(d1[g + 1]) * 254 + static_cast<int>(d2[g + 1]));
+            const u64x s0 = add2(pk2(__uint_as_float(d0[g] + 0x4B400000u), __uint_as_float(d0[g + 1] + 0x4B400000u)), m2);
+            const u64x xg = fma2(pk2(xe0, xe1), k2, s0);
+            u64x d;
+            if (form > 0) {
+              float v0, v1;
+              upk2(fma2(mx2, xg, mul2(my2, pk2(qs[g], qs[g + 1]))), v0, v1);
+              d = add2(pk2(capped(a, v0, form == 2), capped(a, v1, form == 2)), pk2(-sub[g], -sub[g + 1]));
+            } else {
+              d = fma2(mx2, xg, fma2(my2, pk2(qs[g], qs[g + 1]), pk2(-sub[g], -sub[g + 1])));
+            }
+            if (newest_first) {
+              const float2 sl = *reinterpret_cast<const float2*>(&sm.slope[hb + g]);
+              d = fma2(pk2(sl.x, sl.y), pk2(dist, dist), d);
+            }
+            upk2(d, out[g], out[g + 1]);
+          }
         }
-      } else if (kHeads == 1) {
-        const int e12 = static_cast<int>(d1[0]) * 254 + static_cast<int>(d2[0]);
-        const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[0]));
-        dg[0] = fmaf(mt.x, xg, fmaf(mt.y, qs[0], -mr[0]));
+      };
+      auto scores = [&](const float (&sub)[kHeads], float (&out)[kHeads]) {
+        if (!kScore || a.softcap == 0.0f)
+          scores_as(0, sub, out);
+        else if (a.softcap_near == 0.0f)
+          scores_as(1, sub, out);
+        else
+          scores_as(2, sub, out);
+      };
+      scores(mr, dg);
+      if (kHeads == 1) {
         dmax = dg[0];
       } else {
-        const u64x mx2 = pk2(mt.x, mt.x), my2 = pk2(mt.y, mt.y);
-        const u64x k2 = pk2(1.0f / 64516.0f, 1.0f / 64516.0f), m2 = pk2(-12582912.0f, -12582912.0f);
 #pragma unroll
-        for (int g = 0; g < (kHeads > 1 ? kHeads : 2); g += 2) {
-          const float xe0 = __int2float_rn(static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]));
-          const float xe1 = __int2float_rn(static_cast<int>(d1[g + 1]) * 254 + static_cast<int>(d2[g + 1]));
-          const u64x s0 = add2(pk2(__uint_as_float(d0[g] + 0x4B400000u), __uint_as_float(d0[g + 1] + 0x4B400000u)), m2);
-          const u64x xg = fma2(pk2(xe0, xe1), k2, s0);
-          const u64x d = fma2(mx2, xg, fma2(my2, pk2(qs[g], qs[g + 1]), pk2(-mr[g], -mr[g + 1])));
-          upk2(d, dg[g], dg[g + 1]);
-          dmax = max3f(dmax, dg[g], dg[g + 1]);
-        }
+        for (int g = 0; g < (kHeads > 1 ? kHeads : 2); g += 2) dmax = max3f(dmax, dg[g], dg[g + 1]);
       }
       const bool flag = valid && (dmax + e > kTrigger);
       // (one vote over all softmax threads, the wide layout's two halves
@@ -1474,12 +1494,18 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
         tmem_wait_ld();
         pick_digits(sr, sr2, d0, d1, d2);
         float sg[kHeads];
+        if constexpr (kScore) {
+          const float none[kHeads] = {};
+          scores(none, sg);
+        }
 #pragma unroll
         for (int g = 0; g < kHeads; ++g) {
           const int gh = hb + g;
-          const int e12 = static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]);
-          const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[g]));
-          sg[g] = kScore ? score_of(g) : fmaf(mt.x, xg, mt.y * qs[g]);
+          if (!kScore) {
+            const int e12 = static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]);
+            const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[g]));
+            sg[g] = fmaf(mt.x, xg, mt.y * qs[g]);
+          }
           float u = valid ? sg[g] + e : -CUDART_INF_F;
 #pragma unroll
           for (int o = 16; o; o >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
