@@ -3,16 +3,19 @@
 //
 // Rows.  The G query heads of a kv head share its keys and values, so the
 // tile of a matrix product is (128 / G tokens) x (G heads): 128 rows, row r =
-// token r / G, head r % G.  A CTA takes two such tiles, 256 / G tokens in a
-// row, and walks the 128-token key tiles that either reads, from the newest
-// to the oldest (with a distance bias the largest scores come first).  Packed
-// this way the two tiles cover 32 tokens at G = 8, so little of the diagonal
-// is computed for nothing, and a prompt of 20 tokens fills its tiles.
+// token r / G, head r % G.  An item is two such tiles, 256 / G tokens in a
+// row; they walk the 128-key tiles that either reads, from the newest to the
+// oldest (with a distance bias the largest scores come first).  Packed this
+// way an item covers 32 tokens at G = 8, so little of the diagonal is computed
+// for nothing, and a prompt of 20 tokens fills its tiles.
 //
-// Roles.  Warps 0-3 and 4-7 are the softmax of tile 0 and 1, a thread per row;
-// warp 8 issues the products, warp 9 the copies (TMA, 128-byte swizzle; K and
-// V tiles of 32 KB through one ring of five).  Tensor memory holds, per tile,
-// the scores S (128 fp32 columns) and the output O (128 columns): all 512.
+// Roles.  One CTA a multiprocessor stays and takes items from a list.  Warps
+// 0-3 and 4-7 are the softmax of tile 0 and 1, a thread per row; warp 8 issues
+// the products, warp 9 the copies (TMA, 128-byte swizzle; K and V tiles of 32
+// KB through one ring of four), warp 10 finds the items ahead of the others,
+// so the next item's copies and first scores run under the last one's output.
+// Tensor memory holds, per tile, the scores S (128 fp32 columns) and the
+// output O (128 columns): all 512.
 //   S = Q K^T: A and B K-major from shared memory;
 //   P = 2^(y - m) overwrites S in 16 bits, O += P V: A from tensor memory, V
 //   as it lies ([token][dim]: MN-major).
@@ -23,8 +26,8 @@
 // threads: S(j) is only issued after PV(j-1), so O is at rest when S(j) has
 // arrived); p is at most 2^8, l the fp32 sum of the unrounded p, and the sums
 // of P V are fp32.  P is rounded to the inputs' type, the only rounding to
-// fewer bits before the output's own: half a step, 2^-9 (bf16) or 2^-12
-// (fp16) relative to p, of either sign, so it averages out over the keys.
+// fewer bits before the output's own: half a step, 2^-8 (bf16) or 2^-11 (fp16)
+// of p, of either sign, so it averages out over the keys.
 //
 // Masked places.  A masked score is replaced, not added to, so nothing that
 // stands in a masked key reaches a row; a masked value is multiplied by p = 0,
@@ -32,10 +35,19 @@
 // while its l is finite looks for one in the masked places of its tiles and,
 // if there is one, is computed again without them (fix_row).
 //
-// Work.  The prompts' lengths are on the device, so the grid is the bound
-// n / (256 / G) + batch per kv head, and each CTA finds its (prompt, tile)
-// by its rank: items are ordered by falling tile index over all prompts, so
-// the longest walks start first.
+// What bounds it.  A step of two tiles and 128 keys is 2048 clocks of the
+// tensor core at its full rate (and of shared memory, which S reads at 128
+// bytes a clock) and 2048 of the MUFU's exponentials.  Measured it takes about
+// 3150: a tile's 2100 from S to P (150 for the loads, 350 for the maximum, 1550
+// for 128 exponentials a thread where the MUFU needs 1024, waits for the
+// stores), then 1050 for half of PV, the next S and two hand-overs.  One prompt
+// of 16384 tokens, 64 and 8 heads, bf16: 3.4 ms, 1290 TFLOP/s, alone, 4.0 ms in
+// a row, where the card's power limit lowers the clock (a library product of
+// 8192^3 gives 1661 and 1385).  Tried, and not faster: a part of the
+// exponentials on the FMA pipe; two threads a row (16 softmax warps); 64-key
+// steps with two S buffers a tile, which hide the hand-overs, but their S reads
+// shared memory half again as often (4.4 ms; with a softcap 0.72 against 0.80 at
+// 8192 tokens); P formed with the old maximum while the new one is found.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -58,6 +70,7 @@ constexpr int kItems = 2;          // items handed out ahead
 constexpr int kItemReaders = kSoftWarps + 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per tile
+constexpr int kEarly = 2;          // quarters of P handed over first (1 and 3 measured no faster)
 constexpr float kLazy = 8.0f;      // log2 of the largest p
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // a device-side wait gives up after one second
 
@@ -76,7 +89,7 @@ struct __align__(1024) Smem {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t s_full[2];  // S of the tile is written (and every product before it is complete)
-  uint64_t p_half[2], p_full[2];  // P of the tile's first 64 keys, of all, is written (O rescaled)
+  uint64_t p_early[2], p_full[2];  // P of the tile's first keys, of all, is written (O rescaled)
   uint64_t o_full[2];  // O of the tile is final
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t fin;        // every product issued is complete
@@ -522,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(&sm.q_full[i], 1);
         mbar_init(&sm.q_empty[i], 1);
         mbar_init(&sm.s_full[i], 1);
-        mbar_init(&sm.p_half[i], kSoftWarps / 2);
+        mbar_init(&sm.p_early[i], kSoftWarps / 2);
         mbar_init(&sm.p_full[i], kSoftWarps / 2);
         mbar_init(&sm.o_full[i], 1);
       }
@@ -691,10 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               const uint64_t y = dv + 2048u * sv;
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
-                wait(hf == 0 ? &sm.p_half[i] : &sm.p_full[i], (pph >> i) & 1u);
+                wait(hf == 0 ? &sm.p_early[i] : &sm.p_full[i], (pph >> i) & 1u);
                 tc_fence_after();
 #pragma unroll
-                for (int s = 4 * hf; s < 4 * hf + 4; ++s)
+                for (int s = hf == 0 ? 0 : 2 * kEarly; s < (hf == 0 ? 2 * kEarly : 8); ++s)
                   mma_ts(elected, tbase + kColO + 128 * i, tbase + kColS + 128 * i + 8 * s, y + 128 * s,
                          idesc<kBF16>(true), started[i] || s > 0);
               }
@@ -820,15 +833,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (lane == 0) mbar_arrive(bar);
         };
         uint32_t v[16];
-        exps(0, v);
-        tmem_st16(ts, v);
-        exps(1, v);
-        tmem_st16(ts + 16, v);
-        hand_over(&sm.p_half[i]);
-        exps(2, v);
-        tmem_st16(ts + 32, v);
-        exps(3, v);
-        tmem_st16(ts + 48, v);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          exps(x, v);
+          tmem_st16(ts + 16 * x, v);
+          if (x == kEarly - 1) hand_over(&sm.p_early[i]);
+        }
         hand_over(&sm.p_full[i]);
       }
       if (!mbar_wait(&sm.o_full[i], oph, abort)) bad = true;
