@@ -478,6 +478,8 @@ def make_score_opts(softmax_scale=0.0, softcap=0.0, window=0, alibi_slopes=None)
     if alibi_slopes is not None:
         if not (alibi_slopes.is_cuda and alibi_slopes.dtype is _need_torch().float32 and alibi_slopes.is_contiguous()):
             _refuse("make_score_opts", "alibi_slopes is a contiguous fp32 device tensor")
+    if not 0 <= window < 2 ** 31:
+        _refuse("make_score_opts", "window")
     o = ScoreOpts(softmax_scale, softcap, window, _addr(alibi_slopes))
     o.slopes_tensor = alibi_slopes
     return o

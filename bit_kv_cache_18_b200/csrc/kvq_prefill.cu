@@ -441,7 +441,9 @@ struct Items {
   const PrefillArgs& a;
   const int lane, log_tokens;
   int mine;   // pairs of prompt `lane` (all that is needed up to 32 prompts)
-  int bound;  // no prompt has more pairs
+  int index;  // the pair index last found (at first: no prompt has so many pairs)
+  int above, upto;  // pairs with a larger index; with that or a larger one
+  int base, seen;   // prompts before `base`, a multiple of 32: `seen` have such a pair
   __device__ __forceinline__ int tiles(int b) const {
     const int s = __ldg(a.cu_seqlens + b), e = __ldg(a.cu_seqlens + b + 1);
     return s >= 0 && e >= s && e <= a.n_tokens ? (e - s + (1 << log_tokens) - 1) >> log_tokens : -1;
@@ -462,36 +464,42 @@ struct Items {
       bad |= n < 0;
       most = max(most, n);
     }
-    bound = __reduce_max_sync(0xffffffffu, most);
+    index = __reduce_max_sync(0xffffffffu, most);
+    above = upto = base = seen = 0;
     if (bad && blockIdx.x == 0) record_status(a.status, KVQ_ERR_OUT_OF_RANGE);
   }
   // the item of rank `rank` among the pairs; false if there is none.  Ranks rise
-  // from call to call, so the index searched for only falls.
+  // from call to call, so the index only falls, and among one index's prompts
+  // the walk goes on where it was.
   __device__ __forceinline__ bool find(int rank, Item* it) {
-    int lo = 0, hi = bound;  // count(lo) > rank >= count(hi)
-    if (rank >= count(0)) return false;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (count(mid) > rank)
-        lo = mid;
-      else
-        hi = mid;
+    if (rank >= upto) {
+      int lo = 0, hi = index;  // count(lo) > rank >= count(hi)
+      if (rank >= count(0)) return false;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (count(mid) > rank)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      index = lo;
+      above = count(lo + 1);
+      upto = count(lo);
+      base = seen = 0;
     }
-    bound = lo + 1;
-    int k = rank - count(lo + 1);  // my place among the prompts with more than lo pairs
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int b = b0 + lane;
-      const uint32_t has = __ballot_sync(0xffffffffu, b < a.batch && (b0 == 0 ? mine : tiles(b)) > lo);
+    for (; base < a.batch; base += 32) {
+      const int b = base + lane, k = rank - above - seen;  // my place among the prompts from base on
+      const uint32_t has = __ballot_sync(0xffffffffu, b < a.batch && (base == 0 ? mine : tiles(b)) > index);
       if (k >= __popc(has)) {
-        k -= __popc(has);
+        seen += __popc(has);
         continue;
       }
       const bool me = ((has >> lane) & 1u) != 0 && __popc(has & ((1u << lane) - 1u)) == k;
-      const int at = b0 + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+      const int at = base + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
       it->row0 = __ldg(a.cu_seqlens + at);
       it->n = __ldg(a.cu_seqlens + at + 1) - it->row0;
       it->prefix = a.prefix_lens != nullptr ? min(__ldg(a.prefix_lens + at), it->n) : 0;
-      it->t0 = lo << log_tokens;
+      it->t0 = index << log_tokens;
       return true;
     }
     return false;

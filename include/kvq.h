@@ -336,10 +336,10 @@ int kvq_decode_attention_window(const kvq_cache_desc* desc, const kvq_window_des
 
 /* Step tables, on the GPU.  Free blocks lie in a ring: `ring` holds
  * `capacity` block ids (each >= 0, at most 2^27 - 2), of which
- * state[1] starting at index state[0] (wrapping) are free, in the order in
- * which they are handed out.  state is four int32 words: head, count, a
- * ticket (zero before the first call; every call leaves it zero) and one
- * reserved.  With all blocks of a pool either free or held by one sequence
+ * state_in[1] starting at index state_in[0] (wrapping) are free, in the order in
+ * which they are handed out.  state_in and state_out are four int32 words:
+ * head, count, a ticket (zero in state_out before its first call; every call
+ * leaves it zero) and one reserved.  With all blocks of a pool either free or held by one sequence
  * and capacity >= their number, the ring never overflows.
  *
  * seq_lens[b] is the present length of sequence b, target_lens[b] the one it

@@ -142,6 +142,22 @@ def test_many_short_prompts(kvq, cuda):
     _run(kvq, [int(x) for x in rng.integers(0, 9, 900)], 4, 2, "bf16")
 
 
+def test_thousands_of_single_tokens(kvq, cuda):
+    """Each attends to itself alone: its output is its value, bit for bit; every fourth prompt is empty."""
+    import torch
+    n = 20011
+    g = torch.Generator(device="cuda").manual_seed(21)
+    q, k, v = _rows(n, 8, "fp16", g), _rows(n, 2, "fp16", g), _rows(n, 2, "fp16", g)
+    lens = np.ones(n * 4 // 3 + 2, np.int32)
+    lens[3::4] = 0
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    cu = cu[:int(np.searchsorted(cu, n)) + 1]
+    out = torch.empty_like(q)
+    kvq.kvq_prefill_attention(q, k, v, torch.from_numpy(cu).cuda(), out, opts=kvq.make_score_opts(window=7))
+    assert torch.equal(out, v.repeat_interleave(4, dim=1))
+    assert kvq.kvq_last_device_status() == 0
+
+
 @pytest.mark.parametrize("group", [1, 8])
 def test_long_prompt(kvq, cuda, group):
     _run(kvq, [5000], group, 1, "bf16", seed=9)

@@ -122,8 +122,13 @@ def test_scored_decode_refusals(kvq):
                                              kvq.KVQ_BF16, batch, hq, one, 1, one, 16, one, kvq.KVQ_F32, ws, nbytes,
                                              None)
 
-    for bad in (dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf), dict(window=-1),
-                dict(softmax_scale=math.nan)):
+    for window in (-1, 2 ** 31, 2 ** 32):
+        with pytest.raises(kvq.KvqError):
+            kvq.make_score_opts(window=window)
+    o = kvq.make_score_opts()
+    o.window = -1
+    assert call(o) == kvq.KVQ_ERR_INVALID
+    for bad in (dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf), dict(softmax_scale=math.nan)):
         assert call(kvq.make_score_opts(**bad)) == kvq.KVQ_ERR_INVALID, bad
     o = kvq.make_score_opts()
     o.alibi_slopes = 0x1002
@@ -163,7 +168,7 @@ def test_prefill_refusals(kvq):
         assert call(**kw) == kvq.KVQ_ERR_INVALID, kw
     for kw in (dict(hq=6), dict(hq=5), dict(hq=32, qs=4096, os=4096), dict(dtype=kvq.KVQ_F32)):
         assert call(**kw) == kvq.KVQ_ERR_UNSUPPORTED, kw
-    for bad in (dict(softcap=-1.0), dict(softcap=math.inf), dict(window=-1), dict(softmax_scale=math.nan)):
+    for bad in (dict(softcap=-1.0), dict(softcap=math.inf), dict(softmax_scale=math.nan)):
         assert call(kvq.make_score_opts(**bad)) == kvq.KVQ_ERR_INVALID, bad
     o = kvq.make_score_opts()
     o.alibi_slopes = 0x1001
