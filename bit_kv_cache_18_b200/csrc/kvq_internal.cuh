@@ -344,7 +344,7 @@ constexpr int kMaxRopeHeads = 65536;
 
 // Attention of whole prompts (kvq_prefill_attention).
 struct PrefillArgs {
-  CUtensorMap map_q, map_k, map_v;  // filled by launch_prefill
+  CUtensorMap map_q, map_k, map_v, map_out;  // filled by launch_prefill
   const uint16_t* q;
   const uint16_t* k;
   const uint16_t* v;

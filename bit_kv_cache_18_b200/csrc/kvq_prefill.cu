@@ -165,6 +165,25 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
+// A box of shared memory to memory, in a group of its own (one thread), and the
+// warp's waits: until its copies have read their shared memory, and until they
+// have written theirs.
+__device__ __forceinline__ void tma_store4(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n"
+      "cp.async.bulk.commit_group;" ::"l"(map),
+      "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void copies_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void copies_done() {
+  asm volatile("cp.async.bulk.wait_group 0;\nfence.proxy.async.global;" ::: "memory");
+  __syncwarp();
+}
+
 // sm_100 shared-memory matrix descriptors with the 128-byte swizzle, version
 // 1: 8 rows of 128 bytes are an atom of 1024.  K-major (Q, K): atoms follow
 // each other along the rows, the leading offset is not used.  MN-major (V):
@@ -530,8 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == kLoadWarp) {
-    if (lane < 3)
-      asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.map_q : lane == 1 ? &a.map_k : &a.map_v) : "memory");
+    if (lane < 4)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &a.map_q : lane == 1 ? &a.map_k : lane == 2 ? &a.map_v : &a.map_out)
+                   : "memory");
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < kStages; ++i) {
@@ -772,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (kCap) cap_scores(s, a);
         if (kBias) {
           const float d0 = static_cast<float>(j0 - t);
-          if (j0 + kTile - 1 <= first) {  // no key behind a query: linear
+          if (sp.prefix <= first + 1) {  // no query reads a key behind it: linear
             const u64x k2 = twice(kCap ? 1.0f : a.scale_log2);
             const u64x sl = twice(slope2), b2 = twice(slope2 * d0);
 #pragma unroll
@@ -785,11 +805,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               s[e] = fmaf(-slope2, fabsf(d0 + static_cast<float>(e)), kCap ? s[e] : s[e] * a.scale_log2);
           }
         }
-        const bool masked = j0 + kTile > sp.hi(first) || j0 < sp.lo(last);
-        if (masked) {
-          const int e0 = lo - j0, e1 = hi - j0;
+        // masked scores, at the newer end and (with a window) at the older one
+        if (j0 + kTile > sp.hi(first)) {
+          const int e1 = hi - j0;
 #pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = e >= e0 && e < e1 ? s[e] : -CUDART_INF_F;
+          for (int e = 0; e < kTile; ++e) s[e] = e < e1 ? s[e] : -CUDART_INF_F;
+        }
+        if (j0 < sp.lo(last)) {
+          const int e0 = lo - j0;
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = e >= e0 ? s[e] : -CUDART_INF_F;
         }
         float mx4[4];  // four chains
 #pragma unroll
@@ -857,44 +882,52 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       l += l1;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       // 64 dims at a time: my row in 16 bits into the warp's staging rows,
-      // 16-byte piece x of row r at x ^ (r % 8); then the warp writes its 32
-      // rows, four at a time
+      // 16-byte piece x of row r at x ^ (r % 8), the copies' 128-byte swizzle;
+      // then one copy writes the warp's 32 rows, or, where some are behind the
+      // last token, the warp does, four at a time.  (Plain stores of all rows
+      // took 1300 clocks a half, the copy runs on its own.)
       uint8_t* stage = sm.out[warp];
+      const int wfirst = first + (((warp & 3) * 32) >> log_g);  // the warp's first token
+      const bool whole = wfirst + (32 >> log_g) <= it.n;
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
         bool finite = true;
-#pragma unroll 1
-        for (int x = 0; x < kHalf / 16; ++x) {
-          float o[16];
-          tmem_ld16(to + kHalf * hf + 16 * x, o);
-          tmem_wait_ld();
+        float o[kHalf];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t v[4];
+        for (int x = 0; x < 2; ++x) tmem_ld32(to + kHalf * hf + 32 * x, o + 32 * x);
+        tmem_wait_ld();
+        copies_read();  // the staging rows are free
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float v0 = o[8 * e + 2 * y] * inv, v1 = o[8 * e + 2 * y + 1] * inv;
-              finite = finite && fabsf(v0) < CUDART_INF_F && fabsf(v1) < CUDART_INF_F;
-              v[y] = pack2<kBF16>(v0, v1);
-            }
-            *reinterpret_cast<uint4*>(stage + lane * kHeadDim + 16 * ((2 * x + e) ^ (lane & 7))) =
-                make_uint4(v[0], v[1], v[2], v[3]);
+        for (int x = 0; x < kHalf / 8; ++x) {
+          uint32_t v[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float v0 = o[8 * x + 2 * y] * inv, v1 = o[8 * x + 2 * y + 1] * inv;
+            finite = finite && fabsf(v0) < CUDART_INF_F && fabsf(v1) < CUDART_INF_F;
+            v[y] = pack2<kBF16>(v0, v1);
           }
+          *reinterpret_cast<uint4*>(stage + lane * kHeadDim + 16 * (x ^ (lane & 7))) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        __syncwarp();
-#pragma unroll 4
-        for (int x = 0; x < 8; ++x) {
-          const int wr = 4 * x + (lane >> 3), row = (warp & 3) * 32 + wr;
-          const int tr = first + (row >> log_g);
-          if (tr < it.n)
-            reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(it.row0 + tr) * a.out_stride +
-                                     ((it.kv_head << log_g) + (row & ((1 << log_g) - 1))) * kHeadDim +
-                                     kHalf * hf)[lane & 7] =
-                *reinterpret_cast<const uint4*>(stage + wr * kHeadDim + 16 * ((lane & 7) ^ (wr & 7)));
+        if (whole) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tma_store4(&a.map_out, smem_u32(stage), 64 * hf, 0, it.kv_head, it.row0 + wfirst);
+        } else {
+          __syncwarp();
+#pragma unroll 1
+          for (int x = 0; x < 8; ++x) {
+            const int wr = 4 * x + (lane >> 3), tr = wfirst + (wr >> log_g);
+            if (tr < it.n)
+              reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(it.row0 + tr) * a.out_stride +
+                                       ((it.kv_head << log_g) + (wr & ((1 << log_g) - 1))) * kHeadDim +
+                                       kHalf * hf)[lane & 7] =
+                  *reinterpret_cast<const uint4*>(stage + wr * kHeadDim + 16 * ((lane & 7) ^ (wr & 7)));
+          }
+          __syncwarp();
         }
-        __syncwarp();
         // rows that a masked value may have spoilt
         uint32_t todo = __ballot_sync(0xffffffffu, valid && !finite && l > 0.0f && l < CUDART_INF_F);
+        if (todo != 0u) copies_done();
         while (todo != 0u) {
           const int src = __ffs(todo) - 1;
           todo &= todo - 1u;
@@ -907,6 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       tc_fence_before();  // O is read: orders the next item's first P, which lets the products write it again
     }
+    copies_done();
   }
   if (bad) record_status(a.status, KVQ_ERR_DEVICE_TIMEOUT);
   tc_fence_before();
@@ -981,6 +1015,7 @@ cudaError_t launch_prefill(PrefillArgs& a, cudaStream_t stream) {
   if (!encode_tiled()) return cudaErrorNotSupported;
   const int group = 1 << a.log_group;
   if (!make_map(&a.map_q, a.q, a.bf16, 4, group, a.num_kv_heads * group, a.n_tokens, a.q_stride, kTile / group) ||
+      !make_map(&a.map_out, a.out, a.bf16, 4, group, a.num_kv_heads * group, a.n_tokens, a.out_stride, 32 / group) ||
       !make_map(&a.map_k, a.k, a.bf16, 3, 1, a.num_kv_heads, a.n_tokens, a.k_stride, kTile) ||
       !make_map(&a.map_v, a.v, a.bf16, 3, 1, a.num_kv_heads, a.n_tokens, a.v_stride, kTile))
     return cudaErrorInvalidValue;

@@ -221,6 +221,20 @@ def test_masked_places_do_not_reach_a_row(kvq, cuda, bad, group):
     assert torch.isfinite(out[250:300][..., keep]).all() and not torch.isfinite(out[250:300, :, 3:5]).any()
 
 
+def test_a_key_that_is_not_a_number_spoils_its_readers(kvq, cuda):
+    """Every query that reads it gets NaN, in the masked tile of the diagonal and in plain ones; the others nothing."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(13)
+    q, k, v = _rows(500, 2, "bf16", g), _rows(500, 2, "bf16", g), _rows(500, 2, "bf16", g)
+    k[130, 0, 7] = float("nan")
+    out = torch.empty_like(q)
+    for opts in (kvq.make_score_opts(), kvq.make_score_opts(softcap=20.0), kvq.make_score_opts(window=200)):
+        kvq.kvq_prefill_attention(q, k, v, torch.tensor([0, 500], dtype=torch.int32, device="cuda"), out, opts=opts)
+        end = 330 if opts.window else 500
+        assert torch.isnan(out[130:end, 0]).all() and torch.isfinite(out[:130]).all() and torch.isfinite(out[:, 1]).all()
+        assert torch.isfinite(out[end:]).all()
+
+
 def test_rows_with_equal_scores(kvq, cuda):
     """Zero queries: the mean of the values."""
     def zero(q, k, v):
