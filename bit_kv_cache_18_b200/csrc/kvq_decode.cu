@@ -1425,60 +1425,51 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
       pick_digits(sr, sr2, d0, d1, d2);
       float dg[kHeads];
       float dmax = -CUDART_INF_F;
-      // the scores of my heads, less sub[g]; (kScore) with the options, dist the
-      // positions from my token to the newest
-      const float dist = kScore ? static_cast<float>(L - 1 - (blk0 * kBlockSize + kChunkTokens * chunk_of(c) + stok)) : 0.0f;
-      // form: 0 no softcap, 1 a softcap, 2 a large one
-      auto scores_as = [&](int form, const float (&sub)[kHeads], float (&out)[kHeads]) {
-        if (kHeads == 1) {
-          const int e12 = static_cast<int>(d1[0]) * 254 + static_cast<int>(d2[0]);
-          const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[0]));
-          if (kScore) {
-            float v = fmaf(mt.x, xg, mt.y * qs[0]);
-            if (form > 0) v = capped(a, v, form == 2);
-            out[0] = fmaf(sm.slope[hb], dist, v) - sub[0];
-          } else {
-            out[0] = fmaf(mt.x, xg, fmaf(mt.y, qs[0], -sub[0]));
-          }
-        } else {
-          const u64x mx2 = pk2(mt.x, mt.x), my2 = pk2(mt.y, mt.y);
-          const u64x k2 = pk2(1.0f / 64516.0f, 1.0f / 64516.0f), m2 = pk2(-12582912.0f, -12582912.0f);
+      // (kScore) dg holds the scores with their options, without the running max,
+      // until after the vote
+      if constexpr (kScore) {
+        // positions from my token to the newest
+        const float dist = static_cast<float>(L - 1 - (blk0 * kBlockSize + kChunkTokens * chunk_of(c) + stok));
+        // form: 0 no softcap, 1 a softcap, 2 a large one
+        auto scores_as = [&](int form) {
 #pragma unroll
-          for (int g = 0; g < (kHeads > 1 ? kHeads : 2); g += 2) {
-            const float xe0 = __int2float_rn(static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]));
-            const float xe1 = __int2float_rn(static_cast<int>(d1[g + 1]) * 254 + static_cast<int>(d2[g + 1]));
-            const u64x s0 = add2(pk2(__uint_as_float(d0[g] + 0x4B400000u), __uint_as_float(d0[g + 1] + 0x4B400000u)), m2);
-            const u64x xg = fma2(pk2(xe0, xe1), k2, s0);
-            u64x d;
-            if (form > 0) {
-              float v0, v1;
-              upk2(fma2(mx2, xg, mul2(my2, pk2(qs[g], qs[g + 1]))), v0, v1);
-              d = add2(pk2(capped(a, v0, form == 2), capped(a, v1, form == 2)), pk2(-sub[g], -sub[g + 1]));
-            } else {
-              d = fma2(mx2, xg, fma2(my2, pk2(qs[g], qs[g + 1]), pk2(-sub[g], -sub[g + 1])));
-            }
-            if (newest_first) {
-              const float2 sl = *reinterpret_cast<const float2*>(&sm.slope[hb + g]);
-              d = fma2(pk2(sl.x, sl.y), pk2(dist, dist), d);
-            }
-            upk2(d, out[g], out[g + 1]);
+          for (int g = 0; g < kHeads; ++g) {
+            const int e12 = static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]);
+            const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[g]));
+            dg[g] = fmaf(mt.x, xg, mt.y * qs[g]);
+            if (form > 0) dg[g] = capped(a, dg[g], form == 2);
           }
-        }
-      };
-      auto scores = [&](const float (&sub)[kHeads], float (&out)[kHeads]) {
-        if (!kScore || a.softcap == 0.0f)
-          scores_as(0, sub, out);
+        };
+        if (a.softcap == 0.0f)
+          scores_as(0);
         else if (a.softcap_near == 0.0f)
-          scores_as(1, sub, out);
+          scores_as(1);
         else
-          scores_as(2, sub, out);
-      };
-      scores(mr, dg);
-      if (kHeads == 1) {
+          scores_as(2);
+        if (newest_first) {
+#pragma unroll
+          for (int g = 0; g < kHeads; ++g) dg[g] = fmaf(sm.slope[hb + g], dist, dg[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < kHeads; ++g) dmax = fmaxf(dmax, dg[g] - mr[g]);
+      } else if (kHeads == 1) {
+        const int e12 = static_cast<int>(d1[0]) * 254 + static_cast<int>(d2[0]);
+        const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[0]));
+        dg[0] = fmaf(mt.x, xg, fmaf(mt.y, qs[0], -mr[0]));
         dmax = dg[0];
       } else {
+        const u64x mx2 = pk2(mt.x, mt.x), my2 = pk2(mt.y, mt.y);
+        const u64x k2 = pk2(1.0f / 64516.0f, 1.0f / 64516.0f), m2 = pk2(-12582912.0f, -12582912.0f);
 #pragma unroll
-        for (int g = 0; g < (kHeads > 1 ? kHeads : 2); g += 2) dmax = max3f(dmax, dg[g], dg[g + 1]);
+        for (int g = 0; g < (kHeads > 1 ? kHeads : 2); g += 2) {
+          const float xe0 = __int2float_rn(static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]));
+          const float xe1 = __int2float_rn(static_cast<int>(d1[g + 1]) * 254 + static_cast<int>(d2[g + 1]));
+          const u64x s0 = add2(pk2(__uint_as_float(d0[g] + 0x4B400000u), __uint_as_float(d0[g + 1] + 0x4B400000u)), m2);
+          const u64x xg = fma2(pk2(xe0, xe1), k2, s0);
+          const u64x d = fma2(mx2, xg, fma2(my2, pk2(qs[g], qs[g + 1]), pk2(-mr[g], -mr[g + 1])));
+          upk2(d, dg[g], dg[g + 1]);
+          dmax = max3f(dmax, dg[g], dg[g + 1]);
+        }
       }
       const bool flag = valid && (dmax + e > kTrigger);
       // (one vote over all softmax threads, the wide layout's two halves
@@ -1489,19 +1480,19 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
         // s + E plus the headroom; the scores are formed again from S (still
         // in tensor memory: it is released below), exactly, without the
         // running max
-        tmem_ld16(my_lanes + kColS + 32 * P, sr);
-        tmem_ld8(my_lanes + kColS + 32 * P + 16, sr2);
-        tmem_wait_ld();
-        pick_digits(sr, sr2, d0, d1, d2);
-        float sg[kHeads];
-        if constexpr (kScore) {
-          const float none[kHeads] = {};
-          scores(none, sg);
+        if constexpr (!kScore) {
+          tmem_ld16(my_lanes + kColS + 32 * P, sr);
+          tmem_ld8(my_lanes + kColS + 32 * P + 16, sr2);
+          tmem_wait_ld();
+          pick_digits(sr, sr2, d0, d1, d2);
         }
+        float sg[kHeads];
 #pragma unroll
         for (int g = 0; g < kHeads; ++g) {
           const int gh = hb + g;
-          if (!kScore) {
+          if constexpr (kScore) {
+            sg[g] = dg[g];
+          } else {
             const int e12 = static_cast<int>(d1[g]) * 254 + static_cast<int>(d2[g]);
             const float xg = fmaf(__int2float_rn(e12), 1.0f / 64516.0f, small_i2f(d0[g]));
             sg[g] = fmaf(mt.x, xg, mt.y * qs[g]);
@@ -1522,7 +1513,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
           alpha[g] = ex2(mr[g] - mn);
           lr[g] *= alpha[g];
           zr[g] *= alpha[g];
-          dg[g] = sg[g] - mn;
+          if (!kScore) dg[g] = sg[g] - mn;
           mr[g] = mn;
         }
         {  // o~ so far in units of the new max
@@ -1545,6 +1536,10 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
         }
         fresh_c = c;
         // the reductions above read sm.red: none writes it again before the next vote
+      }
+      if constexpr (kScore) {
+#pragma unroll
+        for (int g = 0; g < kHeads; ++g) dg[g] -= mr[g];
       }
       tc_fence_before();
       __syncwarp();
