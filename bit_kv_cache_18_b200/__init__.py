@@ -8,6 +8,7 @@ missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -353,7 +354,7 @@ def _refuse(what: str, why: str):
 
 def _on_device(what: str, *tensors) -> int:
     """The current CUDA device, where the launch goes and every tensor has to be."""
-    dev = (_torch or _need_torch()).cuda.current_device()
+    dev = (_torch or _need_torch())._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             _refuse(what, "a tensor is not on the current CUDA device")
@@ -370,13 +371,18 @@ def _all_int32(what: str, *tensors):
 def _rows(what: str, t):
     """[n, heads, 128] with contiguous heads -> n, heads, elements from one
     token's row to the next (any value does for a single row)."""
-    if t.dim() != 3:
+    try:
+        n, heads, d = t.shape
+    except ValueError:
+        d = 0
+    if d != HEAD_DIM:
         _refuse(what, "rows are [tokens, heads, 128]")
-    n, heads, d = t.shape
-    st = t.stride()
-    if d != HEAD_DIM or (n * heads > 0 and (st[2] != 1 or (heads > 1 and st[1] != HEAD_DIM))):
+    if t.is_contiguous():
+        return n, heads, heads * HEAD_DIM
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != HEAD_DIM):
         _refuse(what, "rows are [tokens, heads, 128] with contiguous heads")
-    return n, heads, st[0] if n > 1 else heads * HEAD_DIM
+    return n, heads, row if n > 1 else heads * HEAD_DIM
 
 
 def _addr(t):
@@ -396,8 +402,11 @@ def kvq_update_tables(ring, state_in, state_out, seq_lens, target_lens, lens_out
     what = "kvq_update_tables"
     every = (ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens, positions, seq_ids,
              slots)
-    dev = _on_device(what, *every)
-    _all_int32(what, *every)
+    dev, i32 = (_torch or _need_torch())._C._cuda_getDevice(), _torch.int32
+    for t in every:
+        if t.get_device() != dev or t.dtype is not i32 or not t.is_contiguous():
+            _on_device(what, t)
+            _all_int32(what, t)
     batch, n = seq_lens.numel(), positions.numel()
     if not (state_in.numel() >= 4 and state_out.numel() >= 4 and target_lens.numel() == batch and
             lens_out.numel() == batch and block_table.dim() == 2 and block_table.shape[0] == batch and
@@ -530,15 +539,25 @@ def new_scored_workspace(num_blocks, num_kv_heads, batch, num_q_heads, max_seq_l
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=64)
+def _desc_image(num_blocks: int, num_kv_heads: int, preset):
+    """A cache descriptor without a pool, as bytes to copy (a few times cheaper
+    than its fields one by one), and the size of its pool."""
+    desc = make_desc(num_blocks, num_kv_heads, preset=preset)
+    return bytes(desc), lib().kvq_cache_bytes(ctypes.byref(desc))
+
+
 def kvq_decode_attention_scored(pool, num_blocks, num_kv_heads, q, block_table, seq_lens, max_seq_len, out, workspace,
                                 opts=None, stream=None, preset=(4, 2)):
     """kvq_decode_attention with score options (make_score_opts); workspace
     from new_scored_workspace() with the same window."""
     what = "kvq_decode_attention_scored"
-    desc = make_desc(num_blocks, num_kv_heads, pool, preset)
     if q.dim() != 3:
         _refuse(what, "q is [batch, heads, 128]")
     batch, hq, d = q.shape
+    image, pool_bytes = _desc_image(num_blocks, num_kv_heads, tuple(preset))
+    desc = CacheDesc.from_buffer_copy(image)
+    desc.pool = pool.data_ptr()
     dev = _on_device(what, pool, q, block_table, seq_lens, out, workspace, _slopes_of(what, opts, hq))
     _all_int32(what, block_table, seq_lens)
     if not (d == HEAD_DIM and q.is_contiguous() and out.is_contiguous() and out.shape == q.shape and
@@ -546,7 +565,7 @@ def kvq_decode_attention_scored(pool, num_blocks, num_kv_heads, q, block_table, 
             seq_lens.numel() == batch and workspace.is_contiguous()):
         _refuse(what, "shapes, types and layout")
     # (a pool of an unsupported preset has no size: the library refuses it below)
-    if not pool.is_contiguous() or pool.numel() * pool.element_size() < lib().kvq_cache_bytes(ctypes.byref(desc)):
+    if not pool.is_contiguous() or pool.numel() * pool.element_size() < pool_bytes:
         _refuse(what, "pool too small")
     rc = lib().kvq_decode_attention_scored(ctypes.byref(desc), ctypes.byref(opts) if opts is not None else None,
                                            q.data_ptr(), _codes[q.dtype], batch, hq, block_table.data_ptr(),
