@@ -460,14 +460,15 @@ __device__ __forceinline__ void fix_row(const PrefillArgs& a, int64_t row0, int 
 struct Items {
   const PrefillArgs& a;
   const int lane, log_tokens;
-  int mine;   // pairs of prompt `lane` (all that is needed up to 32 prompts)
-  int index;  // the pair index last found (at first: no prompt has so many pairs)
-  int above, upto;  // pairs with a larger index; with that or a larger one
-  int base, seen;   // prompts before `base`, a multiple of 32: `seen` have such a pair
-  __device__ __forceinline__ int tiles(int b) const {
-    const int s = __ldg(a.cu_seqlens + b), e = __ldg(a.cu_seqlens + b + 1);
+  int row0, n, mine;  // prompt `lane`: first row, length, pairs (all that is needed up to 32 prompts)
+  int total;          // pairs of all prompts
+  int index;          // the pair index last found (at first: no prompt has so many pairs)
+  int above, upto;    // pairs with a larger index; with that or a larger one
+  int base, seen;     // prompts before `base`, a multiple of 32: `seen` have such a pair
+  __device__ __forceinline__ int tiles(int s, int e) const {
     return s >= 0 && e >= s && e <= a.n_tokens ? (e - s + (1 << log_tokens) - 1) >> log_tokens : -1;
   }
+  __device__ __forceinline__ int tiles(int b) const { return tiles(__ldg(a.cu_seqlens + b), __ldg(a.cu_seqlens + b + 1)); }
   // pairs with an index >= i
   __device__ __forceinline__ int count(int i) const {
     int c = max(mine - i, 0);
@@ -475,16 +476,23 @@ struct Items {
     return __reduce_add_sync(0xffffffffu, c);
   }
   __device__ __forceinline__ Items(const PrefillArgs& args, int log_t)
-      : a(args), lane(threadIdx.x & 31), log_tokens(log_t), mine(0) {
-    bool bad = false;
-    int most = 0;
-    for (int b = lane; b < a.batch; b += 32) {
-      const int n = tiles(b);
-      if (b < 32) mine = n;
-      bad |= n < 0;
-      most = max(most, n);
+      : a(args), lane(threadIdx.x & 31), log_tokens(log_t), row0(0), n(0), mine(0) {
+    if (lane < a.batch) {
+      const int e = __ldg(a.cu_seqlens + lane + 1);
+      row0 = __ldg(a.cu_seqlens + lane);
+      n = e - row0;
+      mine = tiles(row0, e);
     }
-    index = __reduce_max_sync(0xffffffffu, most);
+    bool bad = mine < 0;
+    int most = mine, sum = max(mine, 0);
+    for (int b = 32 + lane; b < a.batch; b += 32) {
+      const int x = tiles(b);
+      bad |= x < 0;
+      most = max(most, x);
+      sum += max(x, 0);
+    }
+    total = __reduce_add_sync(0xffffffffu, sum);
+    index = max(__reduce_max_sync(0xffffffffu, most), 0);
     above = upto = base = seen = 0;
     if (bad && blockIdx.x == 0) record_status(a.status, KVQ_ERR_OUT_OF_RANGE);
   }
@@ -493,18 +501,21 @@ struct Items {
   // the walk goes on where it was.
   __device__ __forceinline__ bool find(int rank, Item* it) {
     if (rank >= upto) {
-      int lo = 0, hi = index;  // count(lo) > rank >= count(hi)
-      if (rank >= count(0)) return false;
+      if (rank >= total) return false;
+      int lo = 0, hi = index, at_lo = total, at_hi = upto;  // at_lo = count(lo) > rank >= at_hi = count(hi)
       while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (count(mid) > rank)
+        const int mid = (lo + hi) >> 1, c = count(mid);
+        if (c > rank) {
           lo = mid;
-        else
+          at_lo = c;
+        } else {
           hi = mid;
+          at_hi = c;
+        }
       }
       index = lo;
-      above = count(lo + 1);
-      upto = count(lo);
+      above = at_hi;
+      upto = at_lo;
       base = seen = 0;
     }
     for (; base < a.batch; base += 32) {
@@ -515,9 +526,14 @@ struct Items {
         continue;
       }
       const bool me = ((has >> lane) & 1u) != 0 && __popc(has & ((1u << lane) - 1u)) == k;
-      const int at = base + __ffs(__ballot_sync(0xffffffffu, me)) - 1;
-      it->row0 = __ldg(a.cu_seqlens + at);
-      it->n = __ldg(a.cu_seqlens + at + 1) - it->row0;
+      const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1, at = base + src;
+      if (base == 0) {
+        it->row0 = __shfl_sync(0xffffffffu, row0, src);
+        it->n = __shfl_sync(0xffffffffu, n, src);
+      } else {
+        it->row0 = __ldg(a.cu_seqlens + at);
+        it->n = __ldg(a.cu_seqlens + at + 1) - it->row0;
+      }
       it->prefix = a.prefix_lens != nullptr ? min(__ldg(a.prefix_lens + at), it->n) : 0;
       it->t0 = index << log_tokens;
       return true;
@@ -949,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_after();
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "n"(kTmemCols));
-  pdl_trigger();  // this CTA holds no tensor memory any more
+  pdl_trigger();  // this CTA holds no tensor memory any more (earlier, ragged prompts took 5% longer)
 }
 
 // ---- tensor maps ----------------------------------------------------------------
