@@ -601,7 +601,7 @@ int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_s
   a.status = device_status_ptr();
   if (!a.status) return KVQ_ERR_CUDA;
   const int64_t items = ((static_cast<int64_t>(n_tokens) * group / 256) + batch) * num_kv_heads;
-  if (items > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  if (items > (int64_t{1} << 30)) return KVQ_ERR_UNSUPPORTED;  // (ranks stay within int32)
   return launch_prefill(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
