@@ -412,11 +412,13 @@ def kvq_update_tables(ring, state_in, state_out, seq_lens, target_lens, lens_out
             lens_out.numel() == batch and block_table.dim() == 2 and block_table.shape[0] == batch and
             cu_seqlens.numel() == batch + 1 and seq_ids.numel() == n and slots.numel() == n):
         _refuse(what, "buffer sizes")
-    rc = lib().kvq_update_tables(ring.data_ptr(), ring.numel(), state_in.data_ptr(), state_out.data_ptr(),
-                                 seq_lens.data_ptr(), target_lens.data_ptr(), lens_out.data_ptr(), batch,
-                                 block_table.data_ptr(), block_table.shape[1], cu_seqlens.data_ptr(), n,
-                                 positions.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(), _stream_of(stream, dev))
-    _check(rc, what)
+    rc = (_lib or lib()).kvq_update_tables(ring.data_ptr(), ring.numel(), state_in.data_ptr(), state_out.data_ptr(),
+                                           seq_lens.data_ptr(), target_lens.data_ptr(), lens_out.data_ptr(), batch,
+                                           block_table.data_ptr(), block_table.shape[1], cu_seqlens.data_ptr(), n,
+                                           positions.data_ptr(), seq_ids.data_ptr(), slots.data_ptr(),
+                                           _stream_of(stream, dev))
+    if rc:
+        raise KvqError(rc, what)
 
 
 ROPE_SCALINGS = ("none", "linear", "ntk", "bands", "yarn")
@@ -476,10 +478,11 @@ def kvq_rope(desc, table, magnitude, positions, q, k=None, q_out=None, k_out=Non
             ok = ok and no == n and ho == hk and k_out.dtype is dtype
     if not ok:
         _refuse(what, "shapes and types")
-    rc = lib().kvq_rope(ctypes.byref(desc), table.data_ptr(), magnitude, positions.data_ptr(), n, q.data_ptr(), qs,
-                        q_out.data_ptr(), qos, hq, _addr(k), ks, _addr(k_out), kos, hk, _codes[dtype],
-                        _stream_of(stream, dev))
-    _check(rc, what)
+    rc = (_lib or lib()).kvq_rope(ctypes.byref(desc), table.data_ptr(), magnitude, positions.data_ptr(), n,
+                                  q.data_ptr(), qs, q_out.data_ptr(), qos, hq, _addr(k), ks, _addr(k_out), kos, hk,
+                                  _codes[dtype], _stream_of(stream, dev))
+    if rc:
+        raise KvqError(rc, what)
 
 
 def make_score_opts(softmax_scale=0.0, softcap=0.0, window=0, alibi_slopes=None) -> ScoreOpts:
@@ -518,10 +521,12 @@ def kvq_prefill_attention(q, k, v, cu_seqlens, out, opts=None, prefix_lens=None,
     if not (batch >= 0 and nq == nk == nv == no and ho == hq and hv == hk and dtype in _codes and k.dtype is dtype and
             v.dtype is dtype and out.dtype is dtype and (prefix_lens is None or prefix_lens.numel() == batch)):
         _refuse(what, "shapes and types")
-    rc = lib().kvq_prefill_attention(ctypes.byref(opts) if opts is not None else None, q.data_ptr(), qs, k.data_ptr(),
-                                     ks, v.data_ptr(), vs, out.data_ptr(), os_, nq, hq, hk, cu_seqlens.data_ptr(),
-                                     batch, _addr(prefix_lens), _codes[dtype], _stream_of(stream, dev))
-    _check(rc, what)
+    rc = (_lib or lib()).kvq_prefill_attention(ctypes.byref(opts) if opts is not None else None, q.data_ptr(), qs,
+                                               k.data_ptr(), ks, v.data_ptr(), vs, out.data_ptr(), os_, nq, hq, hk,
+                                               cu_seqlens.data_ptr(), batch, _addr(prefix_lens), _codes[dtype],
+                                               _stream_of(stream, dev))
+    if rc:
+        raise KvqError(rc, what)
 
 
 def kvq_decode_scored_workspace_bytes(num_blocks, num_kv_heads, batch, num_q_heads, max_seq_len, window=0,
@@ -567,12 +572,15 @@ def kvq_decode_attention_scored(pool, num_blocks, num_kv_heads, q, block_table, 
     # (a pool of an unsupported preset has no size: the library refuses it below)
     if not pool.is_contiguous() or pool.numel() * pool.element_size() < pool_bytes:
         _refuse(what, "pool too small")
-    rc = lib().kvq_decode_attention_scored(ctypes.byref(desc), ctypes.byref(opts) if opts is not None else None,
-                                           q.data_ptr(), _codes[q.dtype], batch, hq, block_table.data_ptr(),
-                                           block_table.shape[1], seq_lens.data_ptr(), max_seq_len, out.data_ptr(),
-                                           _codes[out.dtype], workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size(), _stream_of(stream, dev))
-    _check(rc, what)
+    rc = (_lib or lib()).kvq_decode_attention_scored(ctypes.byref(desc),
+                                                     ctypes.byref(opts) if opts is not None else None, q.data_ptr(),
+                                                     _codes[q.dtype], batch, hq, block_table.data_ptr(),
+                                                     block_table.shape[1], seq_lens.data_ptr(), max_seq_len,
+                                                     out.data_ptr(), _codes[out.dtype], workspace.data_ptr(),
+                                                     workspace.numel() * workspace.element_size(),
+                                                     _stream_of(stream, dev))
+    if rc:
+        raise KvqError(rc, what)
 
 
 def kvq_selftest_wait_timeout(limit_us: int, elapsed_ns=None, stream=None):
