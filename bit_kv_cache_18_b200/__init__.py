@@ -396,7 +396,8 @@ def _stream_of(stream, dev: int):
 def kvq_update_tables(ring, state_in, state_out, seq_lens, target_lens, lens_out, block_table, cu_seqlens, positions,
                       seq_ids, slots, stream=None):
     """Block tables and slot maps of a step from its request lengths: int32
-    device tensors ring [capacity], state_in and state_out [4], seq_lens,
+    device tensors ring [capacity], state_in and state_out [4] (head, count,
+    two words that are zero at first; they may be one tensor), seq_lens,
     target_lens and lens_out [batch], block_table [batch, max_blocks],
     cu_seqlens [batch + 1], positions, seq_ids and slots [max_tokens]."""
     what = "kvq_update_tables"

@@ -207,6 +207,8 @@ __device__ __forceinline__ void quantize_vector_warp(const uint8_t* src, uint8_t
 // allocated already or finished.  Shared memory backs this up: no SM can
 // hold three CTAs of these kernels at once (each asks for more than a third
 // of the SM's 228 KB), so at most two 256-column allocations meet on an SM.
+// The prompt attention allocates all 512 columns and its 225 KB leave room for
+// none of the others; it triggers after its deallocation.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
