@@ -30,10 +30,11 @@
 // of p, of either sign, so it averages out over the keys.
 //
 // Masked places.  A masked score is replaced, not added to, so nothing that
-// stands in a masked key reaches a row; a masked value is multiplied by p = 0,
-// which only a NaN or an infinity survives.  A row that ends up not finite
-// while its l is finite looks for one in the masked places of its tiles and,
-// if there is one, is computed again without them (fix_row).
+// stands in a masked key reaches a row.  Values behind the prompt's end are
+// zeroed in shared memory; other masked ones are multiplied by p = 0, which
+// only a NaN or an infinity survives: a row that ends up not finite while its l
+// is finite looks for one in the masked places of its tiles and, if there is
+// one, is computed again without them (fix_row).
 //
 // What bounds it.  A step of two tiles and 128 keys is 2048 clocks of the
 // tensor core at its full rate (and of shared memory, which S reads at 128
@@ -435,17 +436,30 @@ __device__ __forceinline__ void fix_row(const PrefillArgs& a, int64_t row0, int 
   if (!found) return;
   const float4 q = four(a.q, a.q_stride, row0 + t, head);
   float2 o = make_float2(0.0f, 0.0f);
-  for (int j = lo; j < hi; ++j) {
-    const float4 k = four(a.k, a.k_stride, row0 + j, kv_head);
-    float s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+  // eight keys at a time: the other warps wait for this one, a second at most
+  for (int j0 = lo; j0 < hi; j0 += 8) {
+    float s[8];
+    float2 v[8];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    float y = a.softcap > 0.0f ? capped(s, a) : s * a.scale_log2;
-    y = fmaf(-slope2, fabsf(static_cast<float>(t - j)), y);
-    const float p = ex2(y - m);
-    const float2 v = value(j);
-    o.x = fmaf(p, v.x, o.x);
-    o.y = fmaf(p, v.y, o.y);
+    for (int u = 0; u < 8; ++u) {
+      const int j = min(j0 + u, hi - 1);
+      const float4 k = four(a.k, a.k_stride, row0 + j, kv_head);
+      v[u] = value(j);
+      s[u] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (j0 + u >= hi) break;
+      float y = a.softcap > 0.0f ? capped(s[u], a) : s[u] * a.scale_log2;
+      y = fmaf(-slope2, fabsf(static_cast<float>(t - j0 - u)), y);
+      const float p = ex2(y - m);
+      o.x = fmaf(p, v[u].x, o.x);
+      o.y = fmaf(p, v[u].y, o.y);
+    }
   }
   const float inv = 1.0f / l;
   *reinterpret_cast<uint32_t*>(a.out + (row0 + t) * a.out_stride + head * kHeadDim + kHalf * hf + 2 * lane) =
@@ -740,6 +754,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint32_t sv = rk.i;
           wait(&sm.kv_full[sv], rk.ph);
           rk.next();
+          // Values behind the prompt's last token belong to another prompt or to
+          // none: zero, so that whatever stands there (their p is 0) is no part
+          // of a product.  (P is not here yet: this costs no time.)
+          const int valid = it.n - (w.top - 1 - c) * kTile;
+          if (valid < kTile) {
+            for (int r = valid + (lane >> 3); r < kTile; r += 4) {
+              uint8_t* row = sm.kv[sv] + r * 128 + 16 * (lane & 7);
+              *reinterpret_cast<uint4*>(row) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(row + kHalfBytes) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
           const bool more = c + 1 < w.steps;
           const uint32_t sk = rk.i;
           if (more) wait(&sm.kv_full[sk], rk.ph);
@@ -951,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const int tx = __shfl_sync(0xffffffffu, t, src), hx = __shfl_sync(0xffffffffu, head, src);
           const float sx = __shfl_sync(0xffffffffu, slope2, src), mx = __shfl_sync(0xffffffffu, m, src);
           const float lx = __shfl_sync(0xffffffffu, l, src);
-          fix_row<kBF16>(a, it.row0, tx, hx, it.kv_head, hf, klo * kTile, min(khi * kTile, a.n_tokens - it.row0),
+          fix_row<kBF16>(a, it.row0, tx, hx, it.kv_head, hf, klo * kTile, min(khi * kTile, it.n),
                          sp.lo(tx), sp.hi(tx), sx, mx, lx);
         }
       }

@@ -221,6 +221,30 @@ def test_masked_places_do_not_reach_a_row(kvq, cuda, bad, group):
     assert torch.isfinite(out[250:300][..., keep]).all() and not torch.isfinite(out[250:300, :, 3:5]).any()
 
 
+def test_a_long_prompt_before_rows_that_are_not_numbers(kvq, cuda):
+    """65536 tokens and then padding full of NaN; and a later token's value that is not finite: the rows before it
+    are formed again within the wait limit."""
+    import torch
+    n = 65536
+    g = torch.Generator(device="cuda").manual_seed(31)
+    q, k, v = _rows(n + 50, 8, "bf16", g), _rows(n + 50, 1, "bf16", g), _rows(n + 50, 1, "bf16", g)
+    cu = torch.tensor([0, n - 70], dtype=torch.int32, device="cuda")
+    want, out = torch.empty_like(q), torch.full_like(q, 7.0)
+    kvq.kvq_prefill_attention(q, k, v, cu, want)
+    for x in (q, k, v):
+        x[n - 70:] = float("nan")
+    kvq.kvq_prefill_attention(q, k, v, cu, out)
+    assert torch.equal(out[:n - 70], want[:n - 70]) and (out[n - 70:] == 7.0).all()
+    v[n - 80] = float("inf")
+    kvq.kvq_prefill_attention(q, k, v, cu, out)
+    assert kvq.kvq_last_device_status() == 0
+    # formed again without the rounding of p: half a step of each output and of p on one side, the latter at most
+    # 2^-8 sum p |v| / sum p <= 2^-8 max |v|
+    a, b = out[:n - 80].double(), want[:n - 80].double()
+    assert ((a - b).abs() <= 2.0 ** -8 * (a.abs() + b.abs() + v[:n - 80].double().abs().max()) + 1e-4).all()
+    assert not torch.isfinite(out[n - 80:n - 70]).any()
+
+
 def test_a_key_that_is_not_a_number_spoils_its_readers(kvq, cuda):
     """Every query that reads it gets NaN, in the masked tile of the diagonal and in plain ones; the others nothing."""
     import torch
