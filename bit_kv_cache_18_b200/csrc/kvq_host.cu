@@ -584,18 +584,19 @@ int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_s
   a.prefix_lens = prefix_lens;
   const float tau = opts->softmax_scale > 0.0f ? opts->softmax_scale : 0.08838834764831844055f;
   a.scale_log2 = tau * 1.4426950408889634074f;
-  a.softcap = opts->softcap * 1.4426950408889634074f;
-  a.cap_inv = opts->softcap > 0.0f ? std::min(tau / opts->softcap, 1e30f) : 0.0f;
-  // (for a cap so small that a coefficient would pass fp32, only a zero counts as near)
-  a.cap_test = a.cap_inv <= 1000.0f ? a.cap_inv : 3e38f;
+  // (caps beyond 1e30 as 1e30, so that the inverse stays a normal number)
+  const float cap = std::min(opts->softcap, 1e30f);
+  a.softcap = cap * 1.4426950408889634074f;
+  a.cap_inv = cap > 0.0f ? std::min(tau / cap, 1e30f) : 0.0f;
   static const double half[4] = {0.99999945103, -0.33326284231, 0.13189939426, -0.044392738432};
   static const double one[7] = {0.99999994865, -0.33332827979, 0.13325076146, -0.05345164637,
                                 0.020279708285, -0.0061943248336, 0.0010380250967};
+  // (the sixth power of 1e-5 keeps the shorter form's last coefficient a normal number)
+  a.cap_half = a.cap_inv >= 1e-5f && a.cap_inv <= 1000.0f ? 0.5f : 0.0f;
   double power = a.scale_log2;
-  for (int x = 0; x < 7; ++x, power *= static_cast<double>(a.cap_inv) * a.cap_inv) {
-    a.cap_one[x] = static_cast<float>(std::min(std::max(power * one[x], -1e38), 1e38));
-    if (x < 4) a.cap_half[x] = static_cast<float>(std::min(std::max(power * half[x], -1e38), 1e38));
-  }
+  for (int x = 0; x < 4; ++x, power *= static_cast<double>(a.cap_inv) * a.cap_inv)
+    a.cap_half_coef[x] = a.cap_half > 0.0f ? static_cast<float>(power * half[x]) : 0.0f;
+  for (int x = 0; x < 7; ++x) a.cap_one_coef[x] = static_cast<float>(a.scale_log2 * one[x]);
   a.window = opts->window;
   a.alibi_slopes = opts->alibi_slopes;
   a.status = device_status_ptr();

@@ -361,8 +361,9 @@ struct PrefillArgs {
   const int32_t* prefix_lens;  // or nullptr
   float scale_log2;            // softmax scale times log2(e)
   float softcap;               // cap log2(e); 0: no cap
-  float cap_inv, cap_test;     // softmax scale / cap; what chooses between the capped score's forms
-  float cap_half[4], cap_one[7];  // coefficients of the capped score for |s / cap| up to 1/2, 1
+  float cap_inv;               // softmax scale / cap
+  float cap_half;              // up to which |s / cap| the shorter form of the capped score is used: 1/2 or 0
+  float cap_half_coef[4], cap_one_coef[7];  // coefficients of its forms up to there (in the raw product), up to 1 (in s / cap)
   int32_t window;
   const float* alibi_slopes;
   int* status;

@@ -327,29 +327,33 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 
 // Softcap: y = cap tanh(s / cap) in base-2 units from the raw product d, by the
 // largest |x|, x = d cap_inv = s / cap, of the warp's rows:
-//   |x| <= 1/2 or 1: y = d T(d^2), T of degree 3 or 6 the interpolation of
+//   |x| <= 1/2 or 1: y = d scale T(x^2), T of degree 3 or 6 the interpolation of
 //     tanh(sqrt u) / sqrt u at the Chebyshev points of [0, 1/4] or [0, 1], off
-//     by 5.5e-7 or 5.2e-8 of itself, so right for caps of any size; five or
-//     eight packed operations a pair of scores, the cap and the softmax scale
-//     in the coefficients;
+//     by 5.5e-7 or 5.2e-8 of itself, so right for caps of any size.  The first
+//     form, the usual one, is a polynomial in d^2, powers of cap_inv in its
+//     coefficients, five packed operations a pair of scores (six in x^2: 3%
+//     of two prompts of 4096 and 2047 tokens); where those powers would leave
+//     fp32's range cap_half is 0 and the second form, in x^2, takes over: nine;
 //   beyond: y = cap (1 - 2 / (e^2x + 1)), off by 2^-22 cap; four of the MUFU's
-//     a pair, 32 clocks a warp where the FMA pipe takes 10 or 16.
+//     a pair, 32 clocks a warp where the FMA pipe takes 10 or 18.
 __device__ __forceinline__ float capped_far(float d, const PrefillArgs& a) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(d * (a.cap_inv * 2.8853900817779268f)) + 1.0f));  // 2^(2x log2 e)
   return fmaf(-2.0f * a.softcap, r, a.softcap);
 }
-template <int kN>
-__device__ __forceinline__ void capped_near(float (&s)[kTile], const float (&coef)[kN]) {
+// s times the polynomial in (s times unit)^2
+template <bool kUnit, int kN>
+__device__ __forceinline__ void capped_near(float (&s)[kTile], const float (&coef)[kN], float unit) {
   u64x c[kN];
 #pragma unroll
   for (int x = 0; x < kN; ++x) c[x] = twice(coef[x]);
+  const u64x unit2 = twice(unit);
 #pragma unroll
   for (int e = 0; e < kTile; e += 2) {
-    const u64x d = pk2(s[e], s[e + 1]), u = mul2(d, d);
+    const u64x d = pk2(s[e], s[e + 1]), x = kUnit ? mul2(d, unit2) : d, u = mul2(x, x);
     u64x p = c[kN - 1];
 #pragma unroll
-    for (int x = kN - 2; x >= 0; --x) p = fma2(p, u, c[x]);
+    for (int k = kN - 2; k >= 0; --k) p = fma2(p, u, c[k]);
     upk2(mul2(d, p), s[e], s[e + 1]);
   }
 }
@@ -357,22 +361,22 @@ __device__ __forceinline__ void cap_scores(float (&s)[kTile], const PrefillArgs&
   float big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int e = 0; e < kTile; e += 2) big[(e >> 1) & 3] = max3f(big[(e >> 1) & 3], fabsf(s[e]), fabsf(s[e + 1]));
-  const float x = fmaxf(max3f(big[0], big[1], big[2]), big[3]) * a.cap_test;
-  if (!__any_sync(0xffffffffu, x > 0.5f)) {
-    capped_near(s, a.cap_half);
+  const float x = fmaxf(max3f(big[0], big[1], big[2]), big[3]) * a.cap_inv;
+  if (!__any_sync(0xffffffffu, x > a.cap_half)) {
+    capped_near<false>(s, a.cap_half_coef, 1.0f);
   } else if (!__any_sync(0xffffffffu, x > 1.0f)) {
-    capped_near(s, a.cap_one);
+    capped_near<true>(s, a.cap_one_coef, a.cap_inv);
   } else {
 #pragma unroll
     for (int e = 0; e < kTile; ++e) s[e] = capped_far(s[e], a);
   }
 }
 __device__ __forceinline__ float capped(float d, const PrefillArgs& a) {
-  if (fabsf(d) * a.cap_test > 1.0f) return capped_far(d, a);
-  const float u = d * d;
-  float p = a.cap_one[6];
+  const float x = d * a.cap_inv, u = x * x;
+  if (u > 1.0f) return capped_far(d, a);
+  float p = a.cap_one_coef[6];
 #pragma unroll
-  for (int x = 5; x >= 0; --x) p = fmaf(p, u, a.cap_one[x]);
+  for (int k = 5; k >= 0; --k) p = fmaf(p, u, a.cap_one_coef[k]);
   return d * p;
 }
 

@@ -174,6 +174,23 @@ def test_large_scores_and_saturated_caps(kvq, cuda):
     _run(kvq, [300], 4, 2, "fp16", softcap=9.0)  # most rows below half of it, below it, some beyond
 
 
+@pytest.mark.parametrize("at", [0.55, 0.75, 0.95])
+@pytest.mark.parametrize("scale,cap", [(1 / 128, 30.0), (1 / 128, 50.0), (0.0, 200.0), (0.0, 1000.0), (0.0, 10000.0)])
+def test_scores_near_their_cap(kvq, cuda, scale, cap, at):
+    """Scores around `at` of the cap, a few units apart, whatever scale / cap is; those of the second key tile are
+    next to one beyond the cap, so equal scores stand in tiles of both forms of the cap."""
+    import torch
+
+    def near(q, k, v):
+        g = torch.Generator(device="cuda").manual_seed(17)
+        tau = scale or 1 / math.sqrt(128)
+        noise = torch.randn(k.shape, device="cuda", generator=g) / (tau * math.sqrt(128))
+        k.copy_(at * cap / (tau * 128) + noise * (torch.arange(len(k), device="cuda") % 3 == 0)[:, None, None])
+        k[130] = -2 * cap / (tau * 128)
+        q.fill_(1.0)
+    _run(kvq, [300, 40], 2, 1, "fp16", mutate=near, softmax_scale=scale, softcap=cap)
+
+
 def test_rising_scores_move_the_maximum(kvq, cuda):
     """Keys of one direction whose length falls with the position: the oldest tile has the largest scores."""
     import torch
