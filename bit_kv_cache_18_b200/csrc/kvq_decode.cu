@@ -823,13 +823,14 @@ __device__ __forceinline__ void window_part(const DecodeArgs& a, uint8_t* smem) 
 // infinity give -1 and 1) is off by 2^-22 of the cap, where the hardware's tanh,
 // 2^-11, would cost a softcap of 50 two percent of every probability; the two
 // MUFU operations hide behind the chunk's other work.  Caps for which that is
-// not enough (softcap_near > 0) take, up to |s| = cap / 2, s T(s^2) with T the
-// interpolation of tanh(sqrt u) / sqrt u at the four Chebyshev points of [0,
-// 1/4]: off by 5.5e-7 of the score itself.
+// not enough (softcap_near > 0) take, up to |s| = cap / 2, s T((s / cap)^2) with
+// T the interpolation of tanh(sqrt u) / sqrt u at the four Chebyshev points of
+// [0, 1/4]: off by 5.5e-7 of the score itself, whatever the cap (in s^2, with
+// powers of the cap in the coefficients, these leave fp32 from caps of 1e6 on).
 __device__ __forceinline__ float capped(const DecodeArgs& a, float s, bool large) {
   if (large && fabsf(s) <= a.softcap_near) {
-    const float u = s * s;
-    return s * fmaf(fmaf(fmaf(a.softcap_coef[2], u, a.softcap_coef[1]), u, a.softcap_coef[0]), u, 0.99999945f);
+    const float x = s * a.softcap_inv, u = x * x;
+    return s * fmaf(fmaf(fmaf(-0.044392738432f, u, 0.13189939426f), u, -0.33326284231f), u, 0.99999945f);
   }
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * a.softcap_exp) + 1.0f));

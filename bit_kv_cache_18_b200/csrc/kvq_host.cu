@@ -381,14 +381,13 @@ int decode_impl(const kvq_cache_desc* desc, const void* q, kvq_dtype q_dtype, in
   a.win_recent = use_win ? win->recent : 0;
   a.nrec = plan.nrec;
   a.score = opts ? 1 : 0;
-  a.softcap = opts ? opts->softcap * 1.4426950408889634074f : 0.0f;
-  a.softcap_exp = opts && opts->softcap > 0.0f ? std::min(2.0f / opts->softcap, 1e38f) : 0.0f;
+  // (caps beyond 1e30 as 1e30, so that the inverse stays a normal number)
+  const float cap = opts ? std::min(opts->softcap, 1e30f) : 0.0f;
+  a.softcap = cap * 1.4426950408889634074f;
+  a.softcap_exp = cap > 0.0f ? std::min(2.0f / cap, 1e38f) : 0.0f;
   // (up to a cap of 1000 the other form's 2^-22 of it is below 2.5e-4 of a probability)
-  const double cap2 = a.softcap;
-  a.softcap_near = cap2 > 1442.7 ? static_cast<float>(0.5 * cap2) : 0.0f;
-  const double coef[3] = {-0.33326284231, 0.13189939426, -0.044392738432};
-  for (int x = 0; x < 3; ++x)
-    a.softcap_coef[x] = a.softcap_near > 0.0f ? static_cast<float>(coef[x] / std::pow(cap2, 2.0 * (x + 1))) : 0.0f;
+  a.softcap_near = a.softcap > 1442.7f ? 0.5f * a.softcap : 0.0f;
+  a.softcap_inv = a.softcap_near > 0.0f ? 1.0f / a.softcap : 0.0f;
   a.score_window = opts ? opts->window : 0;
   a.alibi_slopes = opts ? opts->alibi_slopes : nullptr;
   if (!a.status) return KVQ_ERR_CUDA;

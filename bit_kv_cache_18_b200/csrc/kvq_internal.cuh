@@ -280,8 +280,8 @@ struct DecodeArgs {
   int32_t score;              // 0: none of the fields below is read
   float softcap;              // cap log2(e); 0: no cap
   float softcap_exp;          // e^(2 s / cap) = 2^(softcap_exp x base-2 score)
-  float softcap_near;         // scores up to this size take the polynomial
-  float softcap_coef[3];
+  float softcap_near;         // scores up to this size take the polynomial in softcap_inv x base-2 score
+  float softcap_inv;
   int32_t score_window;       // positions a query reads; 0: all
   const float* alibi_slopes;  // [num_q_heads] or nullptr
 };

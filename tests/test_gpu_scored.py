@@ -139,6 +139,27 @@ def test_caps_of_any_size(kvq, cuda, softcap):
     _run(kvq, _wl([500, 33], 16, 2, 96), softcap=softcap)
 
 
+@pytest.mark.parametrize("q_mul", [1e4, 3e6, 1e9])
+def test_two_scores_around_half_of_a_large_cap(kvq, cuda, q_mul):
+    """Nearly equal keys, the best just beyond half of the cap and the second just below: both forms of the cap keep
+    their order, so the best takes everything."""
+    import torch
+    wl = _wl([300], 1, 1, 97)
+    g = oracle.geom(num_blocks=wl.num_blocks, num_kv_heads=1, k_bits=8, v_bits=4)
+    pool = oracle.new_pool(g)
+    k, v = wl.kv_rows(synth.TID_K, 0, 300).copy(), wl.kv_rows(synth.TID_V, 0, 300)
+    k[:] = k[:1] ^ np.random.default_rng(2).integers(0, 2, k.shape).astype(k.dtype)  # the last bit of some elements
+    assert oracle.quantize_append(g, pool, k, v, wl.dtype, wl.slots()) == 0
+    kk = _rows(wl, pool, wl.slots(), (8, 4))[0][:, 0]
+    q = torch.from_numpy(q_mul * kk[0] / np.abs(kk[0]).max()).float().view(1, 1, 128)
+    s = np.sort(kk @ q.double().numpy()[0, 0] / math.sqrt(128))
+    cap = float(np.float32(s[-1] + s[-2]))
+    assert 1e-5 < s[-1] / s[-2] - 1 < 1e-3
+    want = _want(wl, pool, q.double().numpy(), (8, 4), softcap=cap)
+    got = _got(kvq, wl, pool, q.cuda(), kvq.make_score_opts(softcap=cap), (8, 4))
+    assert np.abs(got.double().cpu().numpy() - want).max() <= helpers.ATTN_TOL
+
+
 def test_steep_and_zero_and_growing_biases(kvq, cuda):
     """A slope that leaves the newest token alone, a slope of zero, one that favours distant tokens."""
     _run(kvq, _wl([900, 33], 8, 1, 92), alibi_slopes=[100.0, 0.0, -0.01, 1e-6, 3.0, 1e30, 0.5, 0.01])
