@@ -326,7 +326,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 }
 
 // Softcap: y = cap tanh(s / cap) in base-2 units from the raw product d, by the
-// largest |x|, x = d cap_inv = s / cap, of the warp's rows:
+// size of x = d cap_inv = s / cap:
 //   |x| <= 1/2 or 1: y = d scale T(x^2), T of degree 3 or 6 the interpolation of
 //     tanh(sqrt u) / sqrt u at the Chebyshev points of [0, 1/4] or [0, 1], off
 //     by 5.5e-7 or 5.2e-8 of itself, so right for caps of any size.  The first
@@ -336,12 +336,26 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 //     fp32's range cap_half is 0 and the second form, in x^2, takes over: nine;
 //   beyond: y = cap (1 - 2 / (e^2x + 1)), off by 2^-22 cap; four of the MUFU's
 //     a pair, 32 clocks a warp where the FMA pipe takes 10 or 18.
+// With a cap up to 1000 (kCap = 1) a row's scores in a tile take one form, by the
+// largest of them: the highest that a row of the warp needs where every row reads
+// every key, else each row its own, found over the scores that it reads, so that
+// what stands in the others reaches no bit of it.  With a larger one (kCap = 2),
+// for which 2^-22 cap is more than 2.4e-4 of a probability, every score takes
+// its own of the last two.
+constexpr float kLargeCap = 1442.7f;  // 1000, base 2
 __device__ __forceinline__ float capped_far(float d, const PrefillArgs& a) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(d * (a.cap_inv * 2.8853900817779268f)) + 1.0f));  // 2^(2x log2 e)
   return fmaf(-2.0f * a.softcap, r, a.softcap);
 }
-// s times the polynomial in (s times unit)^2
+__device__ __forceinline__ float capped(float d, const PrefillArgs& a) {
+  const float x = d * a.cap_inv, u = x * x;
+  float p = a.cap_one_coef[6];
+#pragma unroll
+  for (int k = 5; k >= 0; --k) p = fmaf(p, u, a.cap_one_coef[k]);
+  return fabsf(x) > 1.0f ? capped_far(d, a) : d * p;
+}
+// s times the polynomial in (s unit)^2 or, without kUnit, in s^2
 template <bool kUnit, int kN>
 __device__ __forceinline__ void capped_near(float (&s)[kTile], const float (&coef)[kN], float unit) {
   u64x c[kN];
@@ -357,27 +371,21 @@ __device__ __forceinline__ void capped_near(float (&s)[kTile], const float (&coe
     upk2(mul2(d, p), s[e], s[e + 1]);
   }
 }
-__device__ __forceinline__ void cap_scores(float (&s)[kTile], const PrefillArgs& a) {
+// live: my row is one of the prompt's; edge: a row of the tile does not read every key (those scores are 0)
+__device__ __forceinline__ void cap_scores(float (&s)[kTile], const PrefillArgs& a, bool live, bool edge) {
   float big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int e = 0; e < kTile; e += 2) big[(e >> 1) & 3] = max3f(big[(e >> 1) & 3], fabsf(s[e]), fabsf(s[e + 1]));
-  const float x = fmaxf(max3f(big[0], big[1], big[2]), big[3]) * a.cap_inv;
-  if (!__any_sync(0xffffffffu, x > a.cap_half)) {
+  float x = live ? fmaxf(max3f(big[0], big[1], big[2]), big[3]) * a.cap_inv : 0.0f;
+  if (!edge) x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+  if (x <= a.cap_half) {
     capped_near<false>(s, a.cap_half_coef, 1.0f);
-  } else if (!__any_sync(0xffffffffu, x > 1.0f)) {
+  } else if (x <= 1.0f) {
     capped_near<true>(s, a.cap_one_coef, a.cap_inv);
   } else {
 #pragma unroll
     for (int e = 0; e < kTile; ++e) s[e] = capped_far(s[e], a);
   }
-}
-__device__ __forceinline__ float capped(float d, const PrefillArgs& a) {
-  const float x = d * a.cap_inv, u = x * x;
-  if (u > 1.0f) return capped_far(d, a);
-  float p = a.cap_one_coef[6];
-#pragma unroll
-  for (int k = 5; k >= 0; --k) p = fmaf(p, u, a.cap_one_coef[k]);
-  return d * p;
 }
 
 // The key interval [lo, hi) of the query at position t of a prompt.
@@ -572,7 +580,7 @@ struct Ring {
   }
 };
 
-template <bool kBF16, bool kCap, bool kBias>
+template <bool kBF16, int kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -837,7 +845,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s + 32 * x);
         tmem_wait_ld();
-        if (kCap) cap_scores(s, a);
+        // The keys that my row reads, a bit each, where a row of the tile does not read
+        // all.  (Comparisons of each score with both ends take more code, of which the
+        // loop has too much: 12 ragged prompts 80.4 us against 78.6.)
+        const bool edge = j0 + kTile > sp.hi(first) || j0 < sp.lo(last);
+        uint32_t reads[4];
+        if (edge) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int from = min(max(lo - j0 - 32 * w, 0), 32), to = min(max(hi - j0 - 32 * w, 0), 32);
+            reads[w] = static_cast<uint32_t>((1ull << to) - 1ull) & ~static_cast<uint32_t>((1ull << from) - 1ull);
+          }
+        }
+        auto mask_with = [&](float x) {
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = (reads[e / 32] >> (e % 32)) & 1u ? s[e] : x;
+        };
+        if (kCap == 1) {
+          if (edge) mask_with(0.0f);  // (for now: the others have no say in the cap's form)
+          cap_scores(s, a, valid, edge);
+        }
+        if (kCap == 2) {
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = capped(s[e], a);
+        }
         if (kBias) {
           const float d0 = static_cast<float>(j0 - t);
           if (sp.prefix <= first + 1) {  // no query reads a key behind it: linear
@@ -853,17 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               s[e] = fmaf(-slope2, fabsf(d0 + static_cast<float>(e)), kCap ? s[e] : s[e] * a.scale_log2);
           }
         }
-        // masked scores, at the newer end and (with a window) at the older one
-        if (j0 + kTile > sp.hi(first)) {
-          const int e1 = hi - j0;
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = e < e1 ? s[e] : -CUDART_INF_F;
-        }
-        if (j0 < sp.lo(last)) {
-          const int e0 = lo - j0;
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = e >= e0 ? s[e] : -CUDART_INF_F;
-        }
+        if (edge) mask_with(-CUDART_INF_F);
         float mx4[4];  // four chains
 #pragma unroll
         for (int x = 0; x < 4; ++x) mx4[x] = fmaxf(s[2 * x], s[2 * x + 1]);
@@ -1040,7 +1061,7 @@ bool make_map(CUtensorMap* map, const void* p, bool bf16, int rank, int inner, i
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kBF16, bool kCap, bool kBias>
+template <bool kBF16, int kCap, bool kBias>
 cudaError_t launch_one(const PrefillArgs& a, cudaStream_t stream) {
   const cudaError_t e = ensure_smem_limit<prefill_kernel<kBF16, kCap, kBias>>(kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1050,11 +1071,14 @@ cudaError_t launch_one(const PrefillArgs& a, cudaStream_t stream) {
   return launch_pdl(prefill_kernel<kBF16, kCap, kBias>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmemBytes,
                     stream, a);
 }
+template <bool kBF16, int kCap>
+cudaError_t launch_cap(const PrefillArgs& a, cudaStream_t stream) {
+  return a.alibi_slopes != nullptr ? launch_one<kBF16, kCap, true>(a, stream) : launch_one<kBF16, kCap, false>(a, stream);
+}
 template <bool kBF16>
 cudaError_t launch_type(const PrefillArgs& a, cudaStream_t stream) {
-  const bool cap = a.softcap > 0.0f, bias = a.alibi_slopes != nullptr;
-  if (cap) return bias ? launch_one<kBF16, true, true>(a, stream) : launch_one<kBF16, true, false>(a, stream);
-  return bias ? launch_one<kBF16, false, true>(a, stream) : launch_one<kBF16, false, false>(a, stream);
+  if (a.softcap > kLargeCap) return launch_cap<kBF16, 2>(a, stream);
+  return a.softcap > 0.0f ? launch_cap<kBF16, 1>(a, stream) : launch_cap<kBF16, 0>(a, stream);
 }
 
 }  // namespace

@@ -238,6 +238,45 @@ def test_masked_places_do_not_reach_a_row(kvq, cuda, bad, group):
     assert torch.isfinite(out[250:300][..., keep]).all() and not torch.isfinite(out[250:300, :, 3:5]).any()
 
 
+@pytest.mark.parametrize("junk", [float("inf"), float("nan"), 3e4])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("softcap", [20.0, 1e5])
+def test_masked_places_do_not_choose_the_form_of_the_cap(kvq, cuda, softcap, window, junk):
+    """Infinities and loud numbers in the keys of later tokens, of tokens before the window, of the next prompt and of
+    padding, and in the padding's queries: every bit of the rows that read none of them is as without them."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(23)
+    q, k, v = _rows(460, 8, "bf16", g), _rows(460, 2, "bf16", g), _rows(460, 2, "bf16", g)
+    cu = torch.tensor([0, 300, 417], dtype=torch.int32, device="cuda")
+    opts = kvq.make_score_opts(softcap=softcap, window=window)
+    want, out = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    kvq.kvq_prefill_attention(q, k, v, cu, want, opts=opts)
+    k[250] = k[400] = junk  # a key in either prompt: rows behind it read it, up to the window
+    k[417:] = q[417:] = junk
+    kvq.kvq_prefill_attention(q, k, v, cu, out, opts=opts)
+    for rows in (slice(0, 250), slice(300, 400)) + ((slice(290, 300),) if window else ()):
+        assert torch.equal(out[rows], want[rows])
+    assert (out[417:] == 7.0).all() and kvq.kvq_last_device_status() == 0
+
+
+def test_a_loud_head_leaves_the_others_their_precision(kvq, cuda):
+    """A cap of 1e5 that one head's scores pass; the others' are a few units: their cap is as good as none, whatever
+    form the loud head's scores in the same tile need."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(29)
+    q, k, v = _rows(300, 4, "fp16", g), _rows(300, 1, "fp16", g), _rows(300, 1, "fp16", g)
+    q[:, 1] *= 400
+    k *= 50
+    q[:, [0, 2, 3]] /= 50
+    out = torch.empty_like(q)
+    cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+    kvq.kvq_prefill_attention(q, k, v, cu, out, opts=kvq.make_score_opts(softcap=2e4))
+    assert (q[:, 1].double() @ k[:, 0].double().T / math.sqrt(128)).abs().max() > 3e4
+    want, tol = _reference(q, k, v, [300], [0], [0])  # tanh(x) is x up to 2e-7 of it for scores below 15
+    for h in (0, 2, 3):
+        _close(out[:, h], want[:, h], tol[:, h])
+
+
 def test_a_long_prompt_before_rows_that_are_not_numbers(kvq, cuda):
     """65536 tokens and then padding full of NaN; and a later token's value that is not finite: the rows before it
     are formed again within the wait limit."""
