@@ -30,11 +30,12 @@
 // of p, of either sign, so it averages out over the keys.
 //
 // Masked places.  A masked score is replaced, not added to, so nothing that
-// stands in a masked key reaches a row.  Values behind the prompt's end are
-// zeroed in shared memory; other masked ones are multiplied by p = 0, which
-// only a NaN or an infinity survives: a row that ends up not finite while its l
-// is finite looks for one in the masked places of its tiles and, if there is
-// one, is computed again without them (fix_row).
+// stands in a masked key reaches a row.  A masked value is multiplied by p = 0,
+// which only a NaN or an infinity survives.  So in the tiles that some row of
+// the item reads only in part (the diagonal's, the window's older end) the
+// products' warp zeroes the values that are not finite and those that no row
+// reads, while the softmax runs; where it met one that is not finite, the rows that
+// read it get it added to their output (add_cleared): no row is formed twice.
 //
 // What bounds it.  A step of two tiles and 128 keys is 2048 clocks of the
 // tensor core at its full rate (and of shared memory, which S reads at 128
@@ -96,6 +97,7 @@ struct __align__(1024) Smem {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t fin;        // every product issued is complete
   Item item[kItems];
+  uint32_t cleared[4];  // number of the last item (from 1, at its remainder by 4) with values that were not finite
   uint32_t tmem_base;
   int abort;           // a wait ran out: every other wait gives up at once
 };
@@ -402,6 +404,8 @@ struct Walk {
   int first[2], last[2];  // tokens of each tile
   int klo[2], khi[2];
   int top, steps;
+  int whole0, whole1;  // the key tiles that every row reads wholly: [whole0, whole1)
+  int newest;          // keys that some row reads: up to here
   bool two;
   __device__ __forceinline__ Walk(const Item& it, int window, int tile_tokens) {
     sp.prefix = it.prefix;
@@ -417,65 +421,129 @@ struct Walk {
     if (!two) khi[1] = klo[1] = klo[0];
     top = max(khi[0], khi[1]);
     steps = top - klo[0];
+    whole0 = (sp.lo(two ? last[1] : last[0]) + kTile - 1) / kTile;
+    whole1 = sp.hi(first[0]) / kTile;
+    newest = sp.hi(two ? last[1] : last[0]);
   }
+  __device__ __forceinline__ bool whole(int j) const { return j >= whole0 && j < whole1; }
   __device__ __forceinline__ bool active(int i, int c) const { return top - 1 - c >= klo[i] && top - 1 - c < khi[i]; }
 };
 
-// 64 dims (half hf) of a row whose output is not finite there though its l is:
-// one warp looks for a value that is not finite among the masked keys [k0, k1)
-// - [lo, hi) that the row's products read, and if there is one forms the output
-// again over [lo, hi).
+// Which of a word's two values are not finite: bits 15 and 31 (one more in an
+// exponent of all ones carries into the sign, which is cleared before).
 template <bool kBF16>
-__device__ __forceinline__ void fix_row(const PrefillArgs& a, int64_t row0, int t, int head, int kv_head, int hf, int k0,
-                                        int k1, int lo, int hi, float slope2, float m, float l) {
-  const int lane = threadIdx.x & 31;
-  auto four = [&](const uint16_t* base, int64_t stride, int64_t r, int h) {
-    const uint2 w = *reinterpret_cast<const uint2*>(base + r * stride + h * kHeadDim + 4 * lane);
-    const float2 x = unpack2<kBF16>(w.x), y = unpack2<kBF16>(w.y);
-    return make_float4(x.x, x.y, y.x, y.y);
-  };
-  auto value = [&](int j) {
-    return unpack2<kBF16>(*reinterpret_cast<const uint32_t*>(a.v + (row0 + j) * a.v_stride + kv_head * kHeadDim +
-                                                             kHalf * hf + 2 * lane));
-  };
-  bool found = false;
-  for (int j = k0; j < k1 && !found; ++j) {
-    if (j == lo) j = hi;
-    if (j >= k1) break;
-    const float2 v = value(j);
-    found = __any_sync(0xffffffffu, !(isfinite(v.x) && isfinite(v.y)));
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & (kBF16 ? 0x7F807F80u : 0x7C007C00u)) + (kBF16 ? 0x00800080u : 0x04000400u)) & 0x80008000u;
+}
+
+// acc + 0 x of two values each: not a number once an x was not finite
+template <bool kBF16>
+__device__ __forceinline__ void add_zero_times(uint32_t& acc, uint32_t x) {
+  if (kBF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+}
+
+// A tile of values that some row of the item reads only in part, as it lies in
+// shared memory: the keys from `rows` on become 0, and so do values of the keys
+// [r0, rows) that are not finite (true if there was one).  One warp, eight lanes
+// a key; it has the time until the tile's P is there, so it looks at 16 keys at a
+// time with one operation a word, and at single values only where that finds
+// something.
+template <bool kBF16>
+__device__ __forceinline__ bool clear_values(uint8_t* tile, int r0, int rows) {
+  const int row = (threadIdx.x & 31) >> 3;
+  uint8_t* at = tile + row * 128 + 16 * (threadIdx.x & 7);
+  uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int r = r0; r < rows; r += 16) {
+    uint4 v[4][2];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        v[x][hf] = make_uint4(0u, 0u, 0u, 0u);
+        if (r + 4 * x + row < rows) v[x][hf] = *reinterpret_cast<const uint4*>(at + (r + 4 * x) * 128 + hf * kHalfBytes);
+      }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        add_zero_times<kBF16>(acc[0], v[x][hf].x);
+        add_zero_times<kBF16>(acc[1], v[x][hf].y);
+        add_zero_times<kBF16>(acc[2], v[x][hf].z);
+        add_zero_times<kBF16>(acc[3], v[x][hf].w);
+      }
   }
-  if (!found) return;
-  const float4 q = four(a.q, a.q_stride, row0 + t, head);
-  float2 o = make_float2(0.0f, 0.0f);
-  // eight keys at a time: the other warps wait for this one, a second at most
-  for (int j0 = lo; j0 < hi; j0 += 8) {
-    float s[8];
-    float2 v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int j = min(j0 + u, hi - 1);
-      const float4 k = four(a.k, a.k_stride, row0 + j, kv_head);
-      v[u] = value(j);
-      s[u] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1)
-#pragma unroll
-      for (int u = 0; u < 8; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (j0 + u >= hi) break;
-      float y = a.softcap > 0.0f ? capped(s[u], a) : s[u] * a.scale_log2;
-      y = fmaf(-slope2, fabsf(static_cast<float>(t - j0 - u)), y);
-      const float p = ex2(y - m);
-      o.x = fmaf(p, v[u].x, o.x);
-      o.y = fmaf(p, v[u].y, o.y);
+  const bool found = __any_sync(0xffffffffu, (not_finite<kBF16>(acc[0]) | not_finite<kBF16>(acc[1]) |
+                                              not_finite<kBF16>(acc[2]) | not_finite<kBF16>(acc[3])) != 0u);
+  if (found) {
+#pragma unroll 1
+    for (int r = r0 + row; r < rows; r += 4) {
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint4* p = reinterpret_cast<uint4*>(at + (r - row) * 128 + hf * kHalfBytes);
+        uint4 v = *p;
+        v.x &= ~((not_finite<kBF16>(v.x) >> 15) * 0xFFFFu);
+        v.y &= ~((not_finite<kBF16>(v.y) >> 15) * 0xFFFFu);
+        v.z &= ~((not_finite<kBF16>(v.z) >> 15) * 0xFFFFu);
+        v.w &= ~((not_finite<kBF16>(v.w) >> 15) * 0xFFFFu);
+        *p = v;
+      }
     }
   }
-  const float inv = 1.0f / l;
-  *reinterpret_cast<uint32_t*>(a.out + (row0 + t) * a.out_stride + head * kHeadDim + kHalf * hf + 2 * lane) =
-      pack2<kBF16>(o.x * inv, o.y * inv);
+#pragma unroll 4
+  for (int r = rows; r < kTile - row; r += 4) {
+    *reinterpret_cast<uint4*>(at + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(at + r * 128 + kHalfBytes) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (found || rows < kTile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return found;
+}
+
+// The values that clear_values took out of key tiles [j0, j1): bit l of up[x]
+// (down[x]) is set if dim 4 l + x of a key that my row reads, one of [lo, hi), is
+// infinite or not a number and not negative (not positive).  One warp, a lane a row.
+template <bool kBF16>
+__device__ __forceinline__ void find_cleared(const PrefillArgs& a, const Item& it, int j0, int j1, int lo, int hi,
+                                             uint32_t (&up)[4], uint32_t (&down)[4]) {
+  const int end = min(j1 * kTile, it.n);
+#pragma unroll 1
+  for (int key = j0 * kTile; key < end; ++key) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.v + (it.row0 + key) * a.v_stride + it.kv_head * kHeadDim) +
+                          (threadIdx.x & 31));
+    if (!__any_sync(0xffffffffu, (not_finite<kBF16>(w.x) | not_finite<kBF16>(w.y)) != 0u)) continue;
+    const float2 f = unpack2<kBF16>(w.x), g = unpack2<kBF16>(w.y);
+    const float v[4] = {f.x, f.y, g.x, g.y};
+    const uint32_t mine = key >= lo && key < hi ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const bool bad = !(fabsf(v[x]) < CUDART_INF_F);
+      up[x] |= __ballot_sync(0xffffffffu, bad && !(v[x] < 0.0f)) & mine;
+      down[x] |= __ballot_sync(0xffffffffu, bad && !(v[x] > 0.0f)) & mine;
+    }
+  }
+}
+
+// An output row's dims that read such values: with its p above 0 an infinity or
+// a NaN decides the sum whatever its factor.
+template <bool kBF16>
+__device__ __forceinline__ void add_cleared(uint16_t* row, const uint32_t (&up)[4], const uint32_t (&down)[4]) {
+#pragma unroll 1
+  for (uint32_t left = up[0] | up[1] | up[2] | up[3] | down[0] | down[1] | down[2] | down[3]; left != 0u; left &= left - 1u) {
+    const int l = __ffs(left) - 1;
+    uint2* at = reinterpret_cast<uint2*>(row) + l;
+    const uint2 w = *at;
+    const float2 f = unpack2<kBF16>(w.x), g = unpack2<kBF16>(w.y);
+    float v[4] = {f.x, f.y, g.x, g.y};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if ((up[x] >> l) & 1u) v[x] += CUDART_INF_F;
+      if ((down[x] >> l) & 1u) v[x] -= CUDART_INF_F;
+    }
+    *at = make_uint2(pack2<kBF16>(v[0], v[1]), pack2<kBF16>(v[2], v[3]));
+  }
 }
 
 // The items of a CTA, found by one warp ahead of the others.  Prompt b has
@@ -616,6 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(&sm.item_empty[i], kItemReaders);
       }
       mbar_init(&sm.fin, 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sm.cleared[i] = 0u;
       sm.abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -711,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // The copies still in flight (after a wait that gave up; else none) land
       // before the CTA gives up its shared memory: the last one into each
       // stage, newest first, and into each query tile.
+#pragma unroll 1
       for (uint32_t x = 0; x < kStages && x < copies; ++x) {
         if (rk.i == 0) {
           rk.i = kStages;
@@ -731,12 +802,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       Ring<kItems> ri;
       Ring<kStages> rk;
       uint32_t pph = 0, qph = 0;  // bit i: parity of tile i's next P, next Q
+      uint32_t number = 0;        // items
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!mbar_wait(bar, parity, abort)) bad = true;
       };
       Item it;
       while (!bad && next_item(ri, &it)) {
         const Walk w(it, a.window, tile_tokens);
+        ++number;
         bool started[2] = {false, false};
         // S of tile i with the keys in `stage`, walked at step c
         auto product_s = [&](int i, uint32_t stage, int c) {
@@ -766,17 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint32_t sv = rk.i;
           wait(&sm.kv_full[sv], rk.ph);
           rk.next();
-          // Values behind the prompt's last token belong to another prompt or to
-          // none: zero, so that whatever stands there (their p is 0) is no part
-          // of a product.  (P is not here yet: this costs no time.)
-          const int valid = it.n - (w.top - 1 - c) * kTile;
-          if (valid < kTile) {
-            for (int r = valid + (lane >> 3); r < kTile; r += 4) {
-              uint8_t* row = sm.kv[sv] + r * 128 + 16 * (lane & 7);
-              *reinterpret_cast<uint4*>(row) = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(row + kHalfBytes) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          const int j = w.top - 1 - c;
+          if (!w.whole(j)) {  // (P is not here yet)
+            // the keys that some row does not read: from the first row's newest on, those
+            // behind the last one's (zeroed unseen); at the window's older end any
+            const int r0 = j < w.whole0 ? 0 : max(w.sp.hi(it.t0) - j * kTile, 0);
+            if (clear_values<kBF16>(sm.kv[sv], r0, min(w.newest - j * kTile, kTile)) && lane == 0)
+              sm.cleared[number & 3u] = number;
             __syncwarp();
           }
           const bool more = c + 1 < w.steps;
@@ -817,11 +886,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int r = tid & (kTile - 1);
     const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t ts = lanes + kColS + 128 * i, to = lanes + kColO + 128 * i;
-    uint32_t sph = 0, oph = 0;
+    uint32_t sph = 0, oph = 0, number = 0;
     Ring<kItems> ri;
     Item it;
     while (!bad && next_item(ri, &it)) {
       const Walk w(it, a.window, tile_tokens);
+      ++number;
       if (i == 1 && !w.two) continue;
       const Span& sp = w.sp;
       const int first = it.t0 + i * tile_tokens, last = min(first + tile_tokens, it.n) - 1;
@@ -960,7 +1030,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const bool whole = wfirst + (32 >> log_g) <= it.n;
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
-        bool finite = true;
         float o[kHalf];
 #pragma unroll
         for (int x = 0; x < 2; ++x) tmem_ld32(to + kHalf * hf + 32 * x, o + 32 * x);
@@ -971,9 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           uint32_t v[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const float v0 = o[8 * x + 2 * y] * inv, v1 = o[8 * x + 2 * y + 1] * inv;
-            finite = finite && fabsf(v0) < CUDART_INF_F && fabsf(v1) < CUDART_INF_F;
-            v[y] = pack2<kBF16>(v0, v1);
+            v[y] = pack2<kBF16>(o[8 * x + 2 * y] * inv, o[8 * x + 2 * y + 1] * inv);
           }
           *reinterpret_cast<uint4*>(stage + lane * kHeadDim + 16 * (x ^ (lane & 7))) = make_uint4(v[0], v[1], v[2], v[3]);
         }
@@ -994,18 +1061,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
           __syncwarp();
         }
-        // rows that a masked value may have spoilt
-        uint32_t todo = __ballot_sync(0xffffffffu, valid && !finite && l > 0.0f && l < CUDART_INF_F);
-        if (todo != 0u) copies_done();
-        while (todo != 0u) {
-          const int src = __ffs(todo) - 1;
-          todo &= todo - 1u;
-          const int tx = __shfl_sync(0xffffffffu, t, src), hx = __shfl_sync(0xffffffffu, head, src);
-          const float sx = __shfl_sync(0xffffffffu, slope2, src), mx = __shfl_sync(0xffffffffu, m, src);
-          const float lx = __shfl_sync(0xffffffffu, l, src);
-          fix_row<kBF16>(a, it.row0, tx, hx, it.kv_head, hf, klo * kTile, min(khi * kTile, it.n),
-                         sp.lo(tx), sp.hi(tx), sx, mx, lx);
-        }
+      }
+      // (Items are at most two ahead of the one whose output is written, so its
+      // number stands.)
+      if (__any_sync(0xffffffffu, *const_cast<volatile uint32_t*>(&sm.cleared[number & 3u]) == number)) {
+        uint32_t up[4] = {0u, 0u, 0u, 0u}, down[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x)  // the older end's tiles, the newer one's
+          find_cleared<kBF16>(a, it, x == 0 ? klo : max(max(w.whole0, w.whole1), klo), x == 0 ? min(w.whole0, khi) : khi, lo,
+                              hi, up, down);
+        copies_done();
+        if (valid) add_cleared<kBF16>(a.out + (it.row0 + t) * a.out_stride + head * kHeadDim, up, down);
       }
       tc_fence_before();  // O is read: orders the next item's first P, which lets the products write it again
     }

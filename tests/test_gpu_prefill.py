@@ -301,6 +301,79 @@ def test_a_long_prompt_before_rows_that_are_not_numbers(kvq, cuda):
     assert not torch.isfinite(out[n - 80:n - 70]).any()
 
 
+@pytest.mark.parametrize("dtype,group,opts", [("bf16", 4, {}), ("fp16", 1, dict(window=150)), ("bf16", 8, dict(softcap=9.0)),
+                                              ("fp16", 2, dict(prefix=200)), ("bf16", 1, dict(window=33, prefix=40))])
+def test_values_that_are_not_finite_reach_their_readers_alone(kvq, cuda, dtype, group, opts):
+    """Infinities and NaN in a few dims of values: an output dim that reads one is as its formula says (infinite, or
+    not a number if it reads a NaN or both infinities), every other one as without them, bit for bit."""
+    import torch
+    lens, inf, nan = [300, 1, 420, 128], float("inf"), float("nan")
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    g = torch.Generator(device="cuda").manual_seed(37)
+    q, k, v = _rows(849, 2 * group, dtype, g), _rows(849, 2, dtype, g), _rows(849, 2, dtype, g)
+    prefixes, o = [opts.get("prefix", 0)] * 4, kvq.make_score_opts(softcap=opts.get("softcap", 0.0),
+                                                                   window=opts.get("window", 0))
+    pre = torch.tensor(prefixes, dtype=torch.int32, device="cuda") if "prefix" in opts else None
+    dcu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    kvq.kvq_prefill_attention(q, k, v, dcu, want, opts=o, prefix_lens=pre)
+    for key, head, dim, x in ((0, 0, 5, inf), (100, 0, 5, -inf), (120, 0, 7, inf), (127, 1, 7, nan), (128, 0, 64, -inf),
+                              (299, 0, 127, nan), (300, 0, 1, inf), (301, 1, 0, nan), (450, 0, 70, inf),
+                              (451, 0, 70, nan), (560, 1, 33, -inf), (720, 1, 33, inf), (721, 0, 2, inf), (848, 1, 90, nan)):
+        v[key, head, dim] = x
+    v[60, 0], v[400:404, 1, 100:] = nan, inf
+    kvq.kvq_prefill_attention(q, k, v, dcu, out, opts=o, prefix_lens=pre)
+    assert kvq.kvq_last_device_status() == 0
+    for s, n, p in zip(cu, lens, prefixes):
+        t, j = torch.arange(n, device="cuda")[:, None], torch.arange(n, device="cuda")[None, :]
+        reads = (j <= t) | (j < p)
+        if o.window:
+            reads &= t - j < o.window
+        vv = v[s:s + n]
+        has = lambda m: torch.einsum("tj,jhd->thd", reads.double(), m.double()) > 0  # noqa: E731
+        up, down, no = has(vv == inf), has(vv == -inf), has(vv.isnan())
+        no |= up & down
+        up, down, no = (x.repeat_interleave(group, 1) for x in (up & ~no, down & ~no, no))
+        got, clean = out[s:s + n], want[s:s + n]
+        assert got[no].isnan().all() and (got[up] == inf).all() and (got[down] == -inf).all()
+        rest = ~(no | up | down)
+        assert torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("bad", ["everywhere", "one dim", "infinite", "last"])
+def test_values_that_are_not_finite_cost_little_time(kvq, cuda, bad):
+    """Values that are NaN throughout, in one dim, infinite throughout, or one of them near a prompt's end: the call
+    takes at most a few times as long (looking at the keys of two or three tiles an item takes each warp some tens of
+    microseconds; forming rows again would take a hundred times as long)."""
+    import torch
+    n = 8192
+    g = torch.Generator(device="cuda").manual_seed(41)
+    q, k, v = _rows(n, 32, "bf16", g), _rows(n, 8, "bf16", g), _rows(n, 8, "bf16", g)
+    cu, out = torch.tensor([0, n], dtype=torch.int32, device="cuda"), torch.empty_like(q)
+
+    def ms():
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        kvq.kvq_prefill_attention(q, k, v, cu, out)
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b)
+    ms()
+    clean = min(ms() for _ in range(3))
+    if bad == "everywhere":
+        v.fill_(float("nan"))
+    elif bad == "one dim":
+        v[:, :, 17] = float("nan")
+    elif bad == "infinite":
+        v.fill_(float("inf"))
+    else:
+        v[n - 2] = float("inf")
+    took = min(ms() for _ in range(2))
+    assert kvq.kvq_last_device_status() == 0
+    assert took <= 12 * clean, (took, clean)
+
+
 def test_a_key_that_is_not_a_number_spoils_its_readers(kvq, cuda):
     """Every query that reads it gets NaN, in the masked tile of the diagonal and in plain ones; the others nothing."""
     import torch
