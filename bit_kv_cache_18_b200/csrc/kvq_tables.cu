@@ -32,6 +32,18 @@ namespace {
 constexpr int kTokensPerCta = 2048;
 constexpr int kSmallThreads = 256, kLargeThreads = 1024;
 
+// The CTAs of a call count themselves in state_out[2] by this step, so that what
+// the word may hold, 0 .. CTAs - 1 steps, is told from anything else, a word
+// that was never zeroed for one: a count that starts elsewhere would find its
+// last CTA too early or never.
+constexpr uint32_t kTicketStep = 0x9E3779B1u;
+constexpr uint32_t inverse(uint32_t x) {  // modulo 2^32, by Newton's iteration (x odd)
+  uint32_t y = x;
+  for (int i = 0; i < 5; ++i) y *= 2u - x * y;
+  return y;
+}
+static_assert(kTicketStep * inverse(kTicketStep) == 1u, "steps to a count");
+
 struct Sums {
   long long need, tok, back;
 };
@@ -82,11 +94,13 @@ __global__ void __launch_bounds__(kLarge ? kLargeThreads : kSmallThreads) tables
   int* backx = needx + a.batch;   // [batch]: blocks returned by them
   __shared__ long long warp_need[32], warp_tok[32], warp_back[32];
   __shared__ long long total_need, total_tok;
-  __shared__ int first_refused, is_last;
+  __shared__ int first_refused, is_last, ticket_bad;
   const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) first_refused = INT_MAX;
   pdl_wait();
   pdl_trigger();
+  const uint32_t ticket =
+      kLarge && gridDim.x > 1 && tid == 0 ? __ldcg(reinterpret_cast<const uint32_t*>(a.state_out + 2)) : 0u;
   int head = a.state_in[0], count = a.state_in[1];
   const bool bad_state = head < 0 || head >= a.capacity || count < 0 || count > a.capacity;
   if (bad_state) {
@@ -151,6 +165,15 @@ __global__ void __launch_bounds__(kLarge ? kLargeThreads : kSmallThreads) tables
     return Sums{__shfl_sync(0xffffffffu, v.need, src), __shfl_sync(0xffffffffu, v.tok, src),
                 __shfl_sync(0xffffffffu, v.back, src)};
   };
+  // (Looked at only now, so that its way from memory costs nothing.)  A bad one is
+  // the same for every CTA: then none counts itself, and every sequence is refused.
+  if (kLarge && tid == 0) {
+    ticket_bad = ticket * inverse(kTicketStep) >= gridDim.x;
+    if (ticket_bad) {
+      first_refused = 0;
+      if (blockIdx.x == 0) record_status(a.status, KVQ_ERR_OUT_OF_RANGE);
+    }
+  }
   const Sums inc = warp_scan(mine);
   if (lane == 31) {
     warp_need[warp] = inc.need;
@@ -193,6 +216,7 @@ __global__ void __launch_bounds__(kLarge ? kLargeThreads : kSmallThreads) tables
   }
   __syncthreads();
   const int refused = first_refused;
+  const bool bad_ticket = kLarge && ticket_bad != 0;
   if (refused >= b0 && refused < b1) {
     run = before;
     bool ok;
@@ -215,7 +239,7 @@ __global__ void __launch_bounds__(kLarge ? kLargeThreads : kSmallThreads) tables
   });
   if (blockIdx.x == 0 && tid == 0) a.cu_seqlens[a.batch] = static_cast<int>(tok);
   // returned blocks that fit the ring (all, unless the caller's counts are off)
-  const int back = static_cast<int>(min(all.back, static_cast<long long>(a.capacity - count)));
+  const int back = bad_ticket ? 0 : static_cast<int>(min(all.back, static_cast<long long>(a.capacity - count)));
   if (back < all.back && blockIdx.x == 0 && tid == 0) record_status(a.status, KVQ_ERR_OUT_OF_RANGE);
   __syncthreads();
 
@@ -280,10 +304,21 @@ __global__ void __launch_bounds__(kLarge ? kLargeThreads : kSmallThreads) tables
 
   // The last CTA writes what may alias an input: every CTA has read it by then.
   __syncthreads();
+  if (bad_ticket) {
+    if (blockIdx.x == 0) {
+      for (int b = tid; b < a.batch; b += nthr) a.lens_out[b] = a.lens[b];
+      if (tid == 0) {
+        const int h = a.state_in[0], c = a.state_in[1];
+        a.state_out[0] = h;
+        a.state_out[1] = c;
+      }
+    }
+    return;
+  }
   if (gridDim.x > 1) {
     if (tid == 0) {
       __threadfence();
-      is_last = atomicAdd(a.state_out + 2, 1) == static_cast<int>(gridDim.x) - 1;
+      is_last = atomicAdd(reinterpret_cast<uint32_t*>(a.state_out + 2), kTicketStep) == (gridDim.x - 1) * kTicketStep;
       __threadfence();
     }
     __syncthreads();

@@ -339,8 +339,11 @@ int kvq_decode_attention_window(const kvq_cache_desc* desc, const kvq_window_des
  * state_in[1] starting at index state_in[0] (wrapping) are free, in the order in
  * which they are handed out.  state_in and state_out are four int32 words:
  * head, count, a ticket (zero in state_out before its first call; every call
- * leaves it zero) and one reserved.  With all blocks of a pool either free or held by one sequence
- * and capacity >= their number, the ring never overflows.
+ * leaves it zero) and one reserved.  A call that needs the ticket (more than
+ * 2048 sequences and max_tokens together) and finds another value leaves every
+ * sequence, the ring and the ticket as they were and records
+ * KVQ_ERR_OUT_OF_RANGE.  With all blocks of a pool either free or held by one
+ * sequence and capacity >= their number, the ring never overflows.
  *
  * seq_lens[b] is the present length of sequence b, target_lens[b] the one it
  * is to have; with have = ceil(seq_lens[b]/16), want = ceil(target_lens[b]/16):

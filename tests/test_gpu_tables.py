@@ -140,6 +140,31 @@ def test_state_outside_the_ring(kvq, cuda, state):
     assert np.array_equal(got[2], lens) and not got[4].any() and (got[5] == -1).all()
 
 
+@pytest.mark.parametrize("ticket", [1 << 20, 1, 5, -1, 147, -2 ** 31])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_ticket_that_is_not_zero_is_recorded(kvq, cuda, ticket, in_place):
+    """State words that were never zeroed, in a call of several CTAs: every sequence is left as it was, no block moves,
+    and it is recorded."""
+    import torch
+    ring, state, lens, target, table = _case(np.random.default_rng(13), 300, 20, 4000, 20)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()  # noqa: E731
+    r, s, n, t, tb = dev(ring), dev([*state, ticket, 0]), dev(lens), dev(target), dev(table)
+    s2 = s if in_place else dev([-9, -9, ticket, 0])
+    n2 = n if in_place else torch.full_like(n, -9)
+    cu, maps = torch.full((301,), -9, dtype=torch.int32, device="cuda"), torch.full((3, 9000), -9, dtype=torch.int32,
+                                                                                   device="cuda")
+    kvq.kvq_update_tables(r, s, s2, n, t, n2, tb, cu, maps[0], maps[1], maps[2])
+    assert kvq.kvq_last_device_status() == kvq.KVQ_ERR_OUT_OF_RANGE
+    assert np.array_equal(r.cpu().numpy(), ring) and np.array_equal(tb.cpu().numpy(), table)
+    assert s2[:2].tolist() == state and np.array_equal(n2.cpu().numpy(), lens)
+    assert not cu.any() and (maps == -1).all()
+    s2[2] = 0  # and then it works
+    kvq.kvq_update_tables(r, s, s2, n, t, n2, tb, cu, maps[0], maps[1], maps[2])
+    want = _reference(ring, state, lens, target, table, 9000)
+    assert kvq.kvq_last_device_status() == 0 and s2[:2].tolist() == want[1] and s2[2].item() == 0
+    assert np.array_equal(n2.cpu().numpy(), np.asarray(want[2])) and np.array_equal(r.cpu().numpy(), want[0])
+
+
 def test_bad_block_ids_give_no_slot(kvq, cuda):
     table = np.array([[3, -1], [134217727, 5]], dtype=np.int32)  # 2^27 - 1: its slots would pass 2^31
     ring = np.array([-2, 4, 9, 9], dtype=np.int32)
