@@ -507,7 +507,8 @@ def _slopes_of(what: str, opts, num_q_heads: int):
 
 
 def kvq_prefill_attention(q, k, v, cu_seqlens, out, opts=None, prefix_lens=None, stream=None):
-    """Attention of whole prompts over their own rows: q and out [n, Hq, 128],
+    """Attention of whole prompts over their own rows, with no history in the
+    cache: q and out [n, Hq, 128],
     k and v [n, Hkv, 128] (fp16 or bf16; slices of a fused projection do),
     cu_seqlens int32 [batch + 1], prefix_lens int32 [batch] or None, opts from
     make_score_opts."""
@@ -555,8 +556,10 @@ def _desc_image(num_blocks: int, num_kv_heads: int, preset):
 
 def kvq_decode_attention_scored(pool, num_blocks, num_kv_heads, q, block_table, seq_lens, max_seq_len, out, workspace,
                                 opts=None, stream=None, preset=(4, 2)):
-    """kvq_decode_attention with score options (make_score_opts); workspace
-    from new_scored_workspace() with the same window."""
+    """kvq_decode_attention with score options (make_score_opts); q[b] is
+    sequence b's query: packed row cu_seqlens[b] of a step whose tables
+    kvq_update_tables made; workspace from new_scored_workspace() with the same
+    window."""
     what = "kvq_decode_attention_scored"
     if q.dim() != 3:
         _refuse(what, "q is [batch, heads, 128]")

@@ -359,8 +359,15 @@ int kvq_decode_attention_window(const kvq_cache_desc* desc, const kvq_window_des
  *     the device status word); so is a sequence one of whose lengths is
  *     outside [0, 16*max_blocks_per_seq] (KVQ_ERR_OUT_OF_RANGE).
  * lens_out[b] is the length that sequence b now has; cu_seqlens [batch+1]
- * the running sum of the new tokens per sequence (the packed batch of
- * kvq_prefill_attention); for packed token n, positions[n], seq_ids[n] and
+ * the running sum of the new tokens per sequence: those of sequence b are the
+ * packed rows cu_seqlens[b] .. cu_seqlens[b+1]-1.  kvq_prefill_attention can
+ * take these bounds where every sequence with new tokens starts from length 0:
+ * it attends within the packed rows alone and would read a longer sequence's
+ * new tokens as a prompt without a history.  A decode's query b is row
+ * cu_seqlens[b]: with one new token for every sequence the packed rows are the
+ * queries as they lie, else (one has ended, waits or was left as it was) the
+ * caller gathers them, in a captured step too.  For packed token n,
+ * positions[n], seq_ids[n] and
  * slots[n] (as in kvq_quantize_append and kvq_window_append), and -1 in all
  * three from cu_seqlens[batch] to max_tokens, so that fixed-size buffers can
  * be used with captured graphs.  state_out gets the new head and count.
@@ -465,9 +472,10 @@ int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_s
                           int32_t n_tokens, int32_t num_q_heads, int32_t num_kv_heads, const int32_t* cu_seqlens,
                           int32_t batch, const int32_t* prefix_lens, kvq_dtype dtype, void* stream);
 
-/* kvq_decode_attention with score options: the query of sequence b stands at
- * position seq_lens[b] - 1.  Blocks that lie wholly before the window are not
- * read (their block_table entries may name blocks given back).  Arguments,
+/* kvq_decode_attention with score options: query b is sequence b's (on packed
+ * rows see kvq_update_tables) and stands at position seq_lens[b] - 1.  Blocks
+ * that lie wholly before the window are not read: their block_table entries
+ * may name blocks given back.  Arguments,
  * status rules and workspace rules are those of kvq_decode_attention; the
  * workspace size is that of kvq_decode_scored_workspace_bytes, which needs
  * the window that the call will use. */

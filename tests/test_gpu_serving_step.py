@@ -142,6 +142,54 @@ def test_prompts_then_captured_decode_steps(kvq, cuda):
         assert sorted(free + owned) == list(range(CAP))
 
 
+def test_decode_queries_gathered_from_the_packed_rows(kvq, cuda):
+    """Steps in which requests end, wait and start: the packed rows behind one without a token move up, so the decode's
+    queries are row cu_seqlens[b] for sequence b, in one graph with the rest.  Every sequence with a new token gets
+    its own attention, an ended one zeros."""
+    import torch
+    batch = 5
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool, ws = kvq.new_pool(CAP, HKV), kvq.new_scored_workspace(CAP, HKV, batch, HQ, WIDTH * B, window=WINDOW)
+    ring, state = torch.arange(CAP, **i32), torch.tensor([0, CAP, 0, 0], **i32)
+    lens, target = torch.zeros(batch, **i32), torch.zeros(batch, **i32)
+    table, cu, maps = torch.full((batch, WIDTH), -1, **i32), torch.zeros(batch + 1, **i32), torch.zeros(3, batch, **i32)
+    desc = kvq.make_rope(128)
+    rope, mag = kvq.new_rope_table(desc)
+    opts = kvq.make_score_opts(softcap=SOFTCAP, window=WINDOW)
+    qkv = torch.zeros(batch, HQ + 2 * HKV, 128, dtype=torch.bfloat16, device="cuda")
+    out, q = torch.zeros(batch, HQ, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(qkv[:, :HQ])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        kvq.kvq_update_tables(ring, state, state, lens, target, lens, table, cu, maps[0], maps[1], maps[2])
+        kvq.kvq_rope(desc, rope, mag, maps[0], qkv[:, :HQ], qkv[:, HQ:HQ + HKV])
+        kvq.kvq_quantize_append(pool, CAP, HKV, qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:], maps[2],
+                                token_stride=(HQ + 2 * HKV) * 128)
+        torch.index_select(qkv[:, :HQ], 0, cu[:-1].clamp(max=batch - 1), out=q)
+        kvq.kvq_decode_attention_scored(pool, CAP, HKV, q, table, lens, WIDTH * B, out, ws, opts)
+    at = [0] * batch
+    # one target per sequence and step: "+" a token more, "." waits, "0" ends
+    for i, step in enumerate(("+++++", "+++++", "+.+0+", "++.++", "0+++.", "+++++")):
+        at = [n + 1 if x == "+" else n if x == "." else 0 for n, x in zip(at, step)]
+        target.copy_(torch.tensor(at, dtype=torch.int32))
+        qkv.copy_(torch.randn(qkv.shape, device="cuda", generator=gen).bfloat16())
+        graph.replay()
+        assert kvq.kvq_last_device_status() == 0 and lens.tolist() == at
+        live = [b for b in range(batch) if step[b] == "+"]
+        assert maps[1].tolist() == live + [-1] * (batch - len(live))
+        bytes_, rows, rotated = pool.cpu().numpy(), table.cpu().numpy(), qkv.double().cpu().numpy()
+        for b in range(batch):
+            if step[b] == "0":
+                assert not out[b].any()
+        for n, b in enumerate(live):
+            ck, cv = _cache_rows(bytes_, rows[b], at[b])
+            w = _attend(rotated[n, :HQ], ck, cv, at[b] - 1)
+            err = np.abs(out[b].double().cpu().numpy() - w) - 2.0 ** -8 * np.abs(w)
+            assert err.max() <= helpers.ATTN_TOL
+
+
 def test_calls_on_several_streams_at_once(kvq, cuda):
     """Prompts, decodes over two pools, writes and tables of different steps side by side: each as it is alone."""
     import torch
