@@ -475,7 +475,9 @@ int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_s
 /* kvq_decode_attention with score options: query b is sequence b's (on packed
  * rows see kvq_update_tables) and stands at position seq_lens[b] - 1.  Blocks
  * that lie wholly before the window are not read: their block_table entries
- * may name blocks given back.  Arguments,
+ * may name blocks that the caller gave to others.  (kvq_update_tables returns
+ * blocks from a row's end only, all of them when the sequence ends: a caller
+ * who gives some back before that returns such a row's blocks itself.)  Arguments,
  * status rules and workspace rules are those of kvq_decode_attention; the
  * workspace size is that of kvq_decode_scored_workspace_bytes, which needs
  * the window that the call will use. */
