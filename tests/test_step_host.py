@@ -173,3 +173,40 @@ def test_prefill_refusals(kvq):
     o = kvq.make_score_opts()
     o.alibi_slopes = 0x1001
     assert call(o) == kvq.KVQ_ERR_INVALID
+
+
+def _exact_turns(dim, base, scaling, factor, length, low, high):
+    """Turns per position of each pair in 60 decimal digits."""
+    from decimal import ROUND_CEILING, ROUND_FLOOR, Decimal as D, getcontext
+    getcontext().prec = 60
+    two_pi = 2 * D("3.14159265358979323846264338327950288419716939937510582097494459")
+    base, factor, low, high = D(base), D(factor), D(low), D(high)
+    if scaling == "ntk":
+        base *= (factor.ln() * dim / (dim - 2)).exp()
+    ramp = [D(0)] * (dim // 2)  # how much of each pair is divided by the factor
+    g = [(base.ln() * (-2 * i) / dim).exp() for i in range(dim // 2)]
+    if scaling == "linear":
+        ramp = [D(1)] * (dim // 2)
+    elif scaling == "bands":
+        ramp = [1 - min(max((length * x / two_pi - low) / (high - low), D(0)), D(1)) for x in g]
+    elif scaling == "yarn":
+        def index(n):
+            return dim * (length / (n * two_pi)).ln() / (2 * base.ln())
+        lo = max(index(high).to_integral_value(ROUND_FLOOR), D(0))
+        hi = min(index(low).to_integral_value(ROUND_CEILING), D(dim - 1))
+        ramp = [min(max((i - lo) / max(hi - lo, D("0.001")), D(0)), D(1)) for i in range(dim // 2)]
+    return [(x * r / factor + x * (1 - r)) / two_pi for x, r in zip(g, ramp)]
+
+
+@pytest.mark.parametrize("dim", [16, 48, 128])
+@pytest.mark.parametrize("scaling,base,factor,length,low,high", [
+    ("none", 10000.0, 1.0, 0, 0, 0), ("none", 1e6, 1.0, 0, 0, 0), ("linear", 10000.0, 4.0, 0, 0, 0),
+    ("ntk", 10000.0, 8.0, 0, 0, 0), ("bands", 500000.0, 8.0, 8192, 1.0, 4.0), ("yarn", 10000.0, 16.0, 4096, 1.0, 32.0)])
+def test_rope_table_in_units_of_its_last_place(kvq, dim, scaling, base, factor, length, low, high):
+    """Extended precision (2^-64 of a value) throughout, then cut to 2^-64: exponent and logarithm of a frequency
+    f < 1 are off by a few 2^-64 of f ln f (at most 0.37), the ramps by as many of (length f / 2 pi) / (high - low), some
+    hundreds for the longest wavelengths that "bands" still blends, times a slope 1 / (high - low) and f below
+    2 pi high / length: within 2^-61 of a turn in all.  A table formed in doubles is off by up to 2^-54."""
+    turns, _ = kvq.kvq_rope_table(kvq.make_rope(dim, base, False, scaling, factor, length, low, high))
+    want = _exact_turns(dim, base, scaling, factor, length, low, high)
+    assert max(abs(int(t) - w * 2 ** 64) for t, w in zip(turns, want)) <= 8
