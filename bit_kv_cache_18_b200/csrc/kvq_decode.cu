@@ -907,7 +907,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, kWide ? 1 : kMinCtasOf
     // orders it after the previous kernel's writes; a stale line prefetched
     // now is updated in L2, the point of coherence, by any later write): the
     // split's block-table slice, the sequence length and, by the block ids
-    // as they read now, the first three chunks' segments.
+    // as they read now, the three oldest chunks' segments: those walked first,
+    // but last where a distance bias has the chunks walked from the newest.
     // (With a sliding window the split's blocks follow from the length: no
     // prefetch.)
     const int pblk0 = blockIdx.x * a.blocks_per_split;

@@ -430,8 +430,10 @@ int kvq_rope_table(const kvq_rope_desc* desc, uint64_t* turns_out, float* magnit
  * NULL).  16-byte aligned pointers, strides >= heads*128 and multiples of 8.
  * turns: the device copy of kvq_rope_table's table for the same desc;
  * positions: device int32 [n_tokens]; the rows of a token with a negative
- * position (padding) are neither read nor written.  Angles are exact to 2^-32
- * of a turn at every position, the arithmetic is fp32, rounded once. */
+ * position (padding) are neither read nor written.  The phase modulo a turn
+ * is formed in fixed point, off by less than 2^-31 of a turn at any position,
+ * and rounded once to fp32, by at most 2^-26 of a turn; the arithmetic is
+ * fp32, rounded once. */
 int kvq_rope(const kvq_rope_desc* desc, const uint64_t* turns, float magnitude, const int32_t* positions,
              int32_t n_tokens, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
              int32_t num_q_heads, const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
