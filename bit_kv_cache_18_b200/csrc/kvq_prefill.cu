@@ -40,13 +40,13 @@
 // What bounds it.  A step of two tiles and 128 keys is 2048 clocks of the
 // tensor core at its full rate (and of shared memory, which S reads at 128
 // bytes a clock) and 2048 of the MUFU's exponentials.  Measured it takes about
-// 3150: a tile's 2100 from S to P (150 for the loads, 350 for the maximum, 1550
+// 3200: a tile's 2100 from S to P (150 for the loads, 350 for the maximum, 1550
 // for 128 exponentials a thread where the MUFU needs 1024, waits for the
 // stores), then 1050 for half of PV, the next S and two hand-overs.  One prompt
-// of 16384 tokens, 64 and 8 heads, bf16: 3.4 ms, 1290 TFLOP/s, alone, 3.9 ms in
+// of 16384 tokens, 64 and 8 heads, bf16: 3.47 ms, 1267 TFLOP/s, alone, 4.0 ms in
 // a row, where the card's power limit lowers the clock (a library product of
 // 8192^3 gives 1661 and 1385).  Twelve ragged prompts of 1 to 1500 tokens, 32 and
-// 8 heads: 84 us, 620 TFLOP/s.  Tried, and not faster: a part of the
+// 8 heads: 81 us, 643 TFLOP/s.  Tried, and not faster: a part of the
 // exponentials on the FMA pipe; two threads a row (16 softmax warps); 64-key
 // steps with two S buffers a tile, which hide the hand-overs, but their S reads
 // shared memory half again as often (4.4 ms; with a softcap 0.72 against 0.80 at

@@ -465,10 +465,11 @@ typedef struct {
  * prefix_lens: device int32 [batch] (cut to [0, n]) or NULL for none.  The
  * rows that belong to no prompt are not written, and what stands in keys and
  * values that a query does not read (infinities and NaN too) does not reach
- * its output.  num_q_heads / num_kv_heads is 1, 2, 4 or 8; pointers 16-byte
+ * its output; one that reads an infinity or a NaN is not finite.  num_q_heads / num_kv_heads is 1, 2, 4 or 8; pointers 16-byte
  * aligned, strides >= heads*128 and multiples of 8; out must not overlap the
  * inputs.  The products' sums, the softmax and its sums are fp32, the
- * probabilities enter the second product in dtype.  One launch, no workspace. */
+ * probabilities enter the second product in dtype (in F16 those below 2^-25 of
+ * a row's largest may drop out of it).  One launch, no workspace. */
 int kvq_prefill_attention(const kvq_score_opts* opts, const void* q, int64_t q_stride, const void* k,
                           int64_t k_stride, const void* v, int64_t v_stride, void* out, int64_t out_stride,
                           int32_t n_tokens, int32_t num_q_heads, int32_t num_kv_heads, const int32_t* cu_seqlens,
